@@ -62,6 +62,8 @@ extern "C" {
 #define KV_DTYPE_BF16 1
 #define KV_DTYPE_F16 2
 #define KV_DTYPE_FP8_E4M3 3  /* K/V pools only: 8-bit E4M3 codes with per-KV-head scales */
+#define KV_DTYPE_INT8 4      /* the *_int8 entry points' pools (8-bit codes, a scale per token and head); no entry
+                                point takes it as an argument */
 
 /* ---- device error bits (OR-ed into *err_flag) --------------------------- */
 #define KV_DEV_ERR_PAGE_RANGE 1  /* a block-table entry outside [0, num_pages); that page is skipped */
@@ -240,6 +242,33 @@ int kv_rope_append(void* k_pages, void* v_pages, void* q_out, const void* q, con
                    int32_t rope_style, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size,
                    int32_t num_pages, int32_t dtype, int* err_flag, void* stream);
 
+/* RMS norm of every query and key head, rotary embedding and KV append in one
+ * pass ([CN-06] 6.1 order, with the per-head norm before the rotation). For
+ * every q row and k row x of Dh values, with its weight w (q_weight / k_weight,
+ * fp32 [Dh]; NULL: all ones):
+ *   y = x * w / sqrt(mean(x^2) + eps),  then rotated as in kv_rope_append;
+ * all in fp32, rounded once to `dtype` (not bit-specified: the sum's order is
+ * the kernel's). v rows are copied. Writes q_out (contiguous [B][H_q][Dh];
+ * q and q_out both NULL: no queries), the k and v rows at slot_mapping[b]
+ * (-1 skips the cache write; a slot past the pool sets KV_DEV_ERR_SLOT), and,
+ * when k_out is not NULL, the k rows to k_out (contiguous [B][H_kv][Dh]) --
+ * for a cache that is written by a quantising append. k_pages, v_pages, v_new
+ * and slot_mapping may be NULL together when k_out is set.
+ *   q_stride, k_stride, v_stride: elements from one token's rows to the next
+ *   (heads of a token are contiguous), so that q, k_new and v_new may be slices
+ *   of one projection's output; at least heads * Dh, a multiple of 16 bytes.
+ *   In place (q_out = q, k_out = k_new) needs the contiguous stride; outputs
+ *   must not overlap inputs otherwise.
+ *   positions, cos_sin, max_pos, rope_style: as kv_rope_append (a position
+ *   outside [0, max_pos) sets KV_DEV_ERR_POSITION, nothing is written for that
+ *   token). eps finite and >= 0. Dh * sizeof(dtype) must be 32 times a power
+ *   of two, at most 1024 (KV_ERR_UNSUPPORTED). dtype F32 / BF16 / F16. */
+int kv_norm_rope_append(void* k_pages, void* v_pages, void* q_out, void* k_out, const void* q, const void* k_new,
+                        const void* v_new, int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* q_weight,
+                        const float* k_weight, float eps, const int64_t* slot_mapping, const int32_t* positions,
+                        const float* cos_sin, int32_t max_pos, int32_t rope_style, int32_t B, int32_t H_q, int32_t H_kv,
+                        int32_t Dh, int32_t page_size, int32_t num_pages, int32_t dtype, int* err_flag, void* stream);
+
 /* One launch for a layer's whole decode step ([CN-06] 6.1 order: rotate q
  * and k by the new token's position, append k and v, attend): as
  * paged_decode_attention_append, with the new token's k row and every query
@@ -378,6 +407,106 @@ int paged_decode_attention_fp8(float* out, const void* q, int32_t q_dtype, const
                                int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
                                int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t num_splits,
                                void* workspace, size_t ws_bytes, int* err_flag, void* stream);
+
+/* ---- int8 K/V cache ----------------------------------------------------
+ * The same 8-bit storage with integer codes and one fp32 scale per token and
+ * KV head, taken from the row itself when it is written: no calibration.
+ * Pools of int8 codes [num_pages][H_kv][P][Dh] and kv_scales, fp32
+ * [num_pages][H_kv][2][P] (K's scales of a (page, head), then V's);
+ * read value = code * scale. */
+
+/* Quantising append: for each b with slot_mapping[b] >= 0, head h and the row
+ * x = k_new[b][h][:] (same for V), with a = max |x|:
+ *   scale = a / 127,  code = rint(x * (127 / a))
+ * (divisions and product rounded to fp32, ties to even: bit-reproducible).
+ * A row with a < 2^-100 is stored as zeros with scale 0; a row holding a NaN or
+ * an infinity gets scale NaN and reads back as NaN. k_new, v_new of src_dtype
+ * (bf16, fp16 or fp32), tokens k_stride / v_stride elements apart (heads
+ * contiguous; at least H_kv * Dh, a multiple of 16 bytes). Dh / 16 must be a
+ * power of two up to 32 (else KV_ERR_UNSUPPORTED). Slots as kv_append. */
+int kv_append_int8(void* k_pages, void* v_pages, float* kv_scales, const void* k_new, const void* v_new,
+                   int64_t k_stride, int64_t v_stride, int32_t src_dtype, const int64_t* slot_mapping, int32_t B,
+                   int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, int* err_flag, void* stream);
+
+/* Reading whole pages back: for i < n, page src_pages[i] of the int8 pools ->
+ * page dst_pages[i] of k_out, v_out ([num_out_pages][H_kv][P][Dh] of out_dtype,
+ * bf16, fp16 or fp32), each value code * scale rounded once. With the pages of
+ * a block table as source, the result serves paged_prefill_attention through a
+ * table of the destination pages. Page ids outside the pools set
+ * KV_DEV_ERR_PAGE_RANGE and skip the pair; destinations must be distinct.
+ * Dh % 16 == 0 (else KV_ERR_UNSUPPORTED). */
+int kv_dequant_pages_int8(void* k_out, void* v_out, int32_t out_dtype, int32_t num_out_pages, const void* k_pages,
+                          const void* v_pages, const float* kv_scales, const int32_t* src_pages,
+                          const int32_t* dst_pages, int32_t n, int32_t H_kv, int32_t Dh, int32_t page_size,
+                          int32_t num_pages, int* err_flag, void* stream);
+
+/* kv_copy_pages for the int8 cache: codes and scales of whole pages (e.g.
+ * after kv_pool_cow_tails). Same conditions and errors; Dh % 16 == 0 and
+ * H_kv * page_size even (else KV_ERR_UNSUPPORTED). */
+int kv_copy_pages_int8(void* k_pages, void* v_pages, float* kv_scales, const int32_t* src_pages,
+                       const int32_t* dst_pages, int32_t n, int32_t H_kv, int32_t Dh, int32_t page_size,
+                       int32_t num_pages, int* err_flag, void* stream);
+
+/* Decode attention over the int8 cache: as paged_decode_attention with
+ * K_t = code * scale, V_t = code * scale (kv_scales 16-byte aligned), q of
+ * q_dtype (KV_DTYPE_BF16 or KV_DTYPE_F16, any finite values). Warp-MMA kernel
+ * only, whatever paged_decode_set_kernel selects (H_q / H_kv <= 64, Dh in
+ * {64, 128}, page_size in {16, 32}, num_pages * H_kv * page_size < 2^31);
+ * num_splits, workspace and errors as paged_decode_attention, the automatic
+ * split count that of E4M3 pools. A block-table entry outside the pool skips
+ * that page only. NaN scales of visible tokens give NaN rows; codes and scales
+ * behind a sequence's length are never used. */
+int paged_decode_attention_int8(float* out, const void* q, int32_t q_dtype, const void* k_pages, const void* v_pages,
+                                const float* kv_scales, const int32_t* block_tables, int32_t max_blocks,
+                                const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
+                                int32_t page_size, int32_t num_pages, float scale, int32_t num_splits, void* workspace,
+                                size_t ws_bytes, int* err_flag, void* stream);
+
+/* ---- modified scores and masks ------------------------------------------
+ * paged_decode_attention and paged_prefill_attention for models whose
+ * attention is not the plain causal softmax. For the query row at position pos
+ * of head h and the key at position t:
+ *   s = scale * q . K_t;
+ *   s = softcap * tanh(s / softcap)               if softcap > 0;
+ *   s = s - alibi_slopes[h] * |pos - t|           if alibi_slopes != NULL
+ *                                                 (device fp32 [H_q], finite);
+ * and the row attends to the keys lo <= t < hi only, with
+ *   lo = max(0, pos - window + 1 (if window > 0), key_start[row] (if given)),
+ *   hi = max(pos + 1, min(prefix_lens[b], seq_lens[b]) (if given)).
+ * key_start: device int32, one per query row ([B] for decode, [q_start[B]]
+ * for prefill): the first token of the row's document, say. prefix_lens:
+ * device int32 [B]: tokens that every row of the sequence's chunk sees, before
+ * or behind its own position (prefill). A row with lo >= hi gets zeros. Keys
+ * that a row does not see have no effect on it, whatever they hold (NaN and
+ * infinities in K and V included); a NaN among the scores or values it sees
+ * gives NaN, an infinity among the values its sign. Pages before the first visible key are not read (their table
+ * entries may be anything).
+ * softcap: 0 (none) or positive and finite; window: 0 (none) or positive.
+ * bf16 / fp16 K/V, H_q / H_kv <= 64, Dh in {64, 128}, page_size in {16, 32},
+ * num_pages * H_kv * page_size < 2^31. */
+
+/* Single-token form: pos = seq_lens[b] - 1. Warp-MMA kernel, whatever
+ * paged_decode_set_kernel selects; num_splits, workspace (the bytes that
+ * paged_decode_workspace_bytes gives for the same arguments) and errors as
+ * paged_decode_attention. With a window the automatic split counts the pages
+ * that a window can touch. */
+int paged_decode_attention_mod(float* out, const void* q, const void* k_pages, const void* v_pages,
+                               const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens, int32_t B,
+                               int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, float scale,
+                               int32_t dtype, float softcap, const float* alibi_slopes, int32_t window,
+                               const int32_t* key_start, int32_t num_splits, void* workspace, size_t ws_bytes,
+                               int* err_flag, void* stream);
+
+/* Chunk form: rows, q_start, max_q_len and errors as paged_prefill_attention
+ * (a bidirectional prefix may reach behind the chunk's rows, never behind
+ * seq_lens[b]). The tcgen05 kernel for Dh = 128 and groups that divide 128
+ * under AUTO and TCGEN05, the warp-MMA kernel otherwise. */
+int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
+                                const void* k_pages, const void* v_pages, const int32_t* block_tables,
+                                int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
+                                int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t dtype,
+                                float softcap, const float* alibi_slopes, int32_t window, const int32_t* key_start,
+                                const int32_t* prefix_lens, int* err_flag, void* stream);
 
 /* Which decode kernel paged_decode_attention uses (process-wide; default AUTO):
  *   KV_DECODE_KERNEL_AUTO  bf16/fp16 K/V, Dh = 128, no fused rotation, and

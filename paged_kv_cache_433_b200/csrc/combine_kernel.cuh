@@ -26,11 +26,14 @@ constexpr int kCombineWarps = 8;
 // first item come from the plan; rows with one chunk were written by the
 // decode kernel and are skipped, empty rows are zeroed here; partial s of
 // (b, query head h) sits at item t0 + s, row h of that item's [g][Dh] block.
-template <int DH, int WPR>
+// MOD: a row's pages are counted from its first visible key (window,
+// key_start), and a NaN sum gives a NaN row.
+template <int DH, int WPR, bool MOD = false>
 __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
     float* __restrict__ out, const float* __restrict__ part_u, const float2* __restrict__ part_ml,
     const int32_t* __restrict__ seq_lens, int32_t B, int32_t H_q, int32_t S, int32_t pages_per_split, int32_t P,
-    int32_t max_blocks, const int32_t* __restrict__ plan, int32_t H_kv) {
+    int32_t max_blocks, const int32_t* __restrict__ plan, int32_t H_kv, int32_t window,
+    const int32_t* __restrict__ key_start) {
     constexpr int kD = DH / 32;  // dims per lane
     constexpr int kPer = 8;      // splits per warp per round
     constexpr int kRound = WPR * kPer;
@@ -47,12 +50,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
     // for the partials, from L2 (ld.global.cg), never from a line an earlier kernel left in this SM's L1.
     int len = 0;
     if (live) len = __ldcg(seq_lens + item / H_q);
+    auto row_pages = [&]() {  // pages of the row that the decode kernel read
+        int n_pages = (len + P - 1) / P;
+        if constexpr (MOD)
+            n_pages -= min(first_visible_key(len - 1, window, key_start, static_cast<int>(item / H_q)), len) / P;
+        return n_pages;
+    };
     int ns = plan != nullptr ? 0 : S;  // splits loaded (grid split: the row's own count masks them after)
     int64_t base = item * S, stride = 1;
     if (live && plan != nullptr) {
         const int b = static_cast<int>(item / H_q);
         if (len < 0 || len > max_blocks * P) len = 0;
-        const int n_pages = (len + P - 1) / P;
+        const int n_pages = row_pages();
         const int C = __ldcg(plan);
         const int items_b = (n_pages + C - 1) / C;
         const int g = H_q / H_kv;
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
         }
         if (plan == nullptr && r0 == 0) {
             if (len < 0 || len > max_blocks * P) len = 0;
-            const int n_pages = (len + P - 1) / P;
+            const int n_pages = live ? row_pages() : 0;
             nrow = min(S, (n_pages + pages_per_split - 1) / pages_per_split);
         }
         float mr = -INFINITY;
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
     }
     if constexpr (WPR == 1) {
         if (live) {
-            const float inv = (L > 0.f) ? 1.f / L : 0.f;
+            const float inv = (MOD ? L != 0.f : L > 0.f) ? 1.f / L : 0.f;
             float* dst = out + item * DH + lane * kD;
             if constexpr (kD == 4) {
                 *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
@@ -160,7 +169,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
                 float U = 0.f;
 #pragma unroll
                 for (int w = 0; w < WPR; ++w) U += sc[w] * red_u[row_w0 + w][d];
-                out[item * DH + d] = (Lt > 0.f) ? U / Lt : 0.f;
+                out[item * DH + d] = (MOD ? Lt != 0.f : Lt > 0.f) ? U / Lt : 0.f;
             }
         }
     }

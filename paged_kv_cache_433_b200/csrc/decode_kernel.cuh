@@ -75,6 +75,15 @@ struct DecodeParams {
     int32_t g, HS, WP;          // GQA group, head slices, page-warps
     int32_t num_splits, pages_per_split;
     float scale_log2;           // scale * log2(e)
+    const float* kv_scales;     // int8 K/V: [num_pages][H_kv][2][P] (K then V)
+    // modified scores and masks (score_mod.cuh)
+    float cap_in, cap_out;      // tanh cap c (cap_out = 0: none): scale / c and c * log2(e)
+    float cap_small;            // products up to this magnitude take the polynomial (negative: none does)
+    float cap_coef[6];          // its coefficients
+    const float* alibi_slopes;  // [H_q] (nullable): bias -slope * |query position - key position|
+    const int32_t* key_start;   // first visible key per query row (nullable)
+    const int32_t* prefix_lens; // multi-token query: keys visible to every row of sequence b (nullable)
+    int32_t window;             // keys visible before and at the row's own position (0: all)
 };
 
 // ---- storage formats ------------------------------------------------------

@@ -81,19 +81,20 @@ cudaError_t launch_decode_f16(const DecodeParams& p, int DH, int P, int GW, int 
 
 namespace kvp {
 
-template <int KT, int QT, int DH, int P, bool LO, bool QM = false>
+template <int KT, int QT, int DH, int P, bool LO, bool QM = false, bool MOD = false>
 cudaError_t launch_mma_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                             cudaStream_t st) {
     constexpr int NW = 4;
-    // E4M3 pages of 16 tokens are half the bytes of a 16-bit page: two of them share a stage
-    constexpr int PPS = (KT == KV_DTYPE_FP8_E4M3 && P == 16) ? 2 : 1;
-    using C = MmaCfg<DH, P, NW, KT == KV_DTYPE_FP8_E4M3 ? 1 : 2, PPS>;
+    // one-byte pages of 16 tokens are half the bytes of a 16-bit page: two of them share a stage
+    constexpr bool k8 = KT == KV_DTYPE_FP8_E4M3 || KT == KV_DTYPE_INT8;
+    constexpr int PPS = (k8 && P == 16) ? 2 : 1;
+    using C = MmaCfg<DH, P, NW, k8 ? 1 : 2, PPS, KT == KV_DTYPE_INT8 ? 8 : 0>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
-    auto* kern = paged_decode_mma_kernel<KT, QT, DH, P, NW, LO, PPS, QM>;
+    auto* kern = paged_decode_mma_kernel<KT, QT, DH, P, NW, LO, PPS, QM, MOD>;
     if (!(configured.load(std::memory_order_acquire) & bit)) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
@@ -106,32 +107,32 @@ cudaError_t launch_mma_inst(const DecodeParams& p, const CUtensorMap& tk, const 
 
 // Groups of at most 8 heads take the instance that carries the probability
 // residual in the MMA's padding rows.
-template <int KT, int QT, int DH, int P>
+template <int KT, int QT, int DH, int P, bool MOD = false>
 cudaError_t launch_mma_group(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                              cudaStream_t st) {
-    return p.g <= 8 ? launch_mma_inst<KT, QT, DH, P, true>(p, tk, tv, grid, st)
-                    : launch_mma_inst<KT, QT, DH, P, false>(p, tk, tv, grid, st);
+    return p.g <= 8 ? launch_mma_inst<KT, QT, DH, P, true, false, MOD>(p, tk, tv, grid, st)
+                    : launch_mma_inst<KT, QT, DH, P, false, false, MOD>(p, tk, tv, grid, st);
 }
 
-template <int KT, int QT>
+template <int KT, int QT, bool MOD = false>
 cudaError_t launch_mma_dt(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int DH, int P, dim3 grid,
                           cudaStream_t st) {
     if (DH == 128)
-        return P == 16 ? launch_mma_group<KT, QT, 128, 16>(p, tk, tv, grid, st)
-                       : launch_mma_group<KT, QT, 128, 32>(p, tk, tv, grid, st);
-    return P == 16 ? launch_mma_group<KT, QT, 64, 16>(p, tk, tv, grid, st)
-                   : launch_mma_group<KT, QT, 64, 32>(p, tk, tv, grid, st);
+        return P == 16 ? launch_mma_group<KT, QT, 128, 16, MOD>(p, tk, tv, grid, st)
+                       : launch_mma_group<KT, QT, 128, 32, MOD>(p, tk, tv, grid, st);
+    return P == 16 ? launch_mma_group<KT, QT, 64, 16, MOD>(p, tk, tv, grid, st)
+                   : launch_mma_group<KT, QT, 64, 32, MOD>(p, tk, tv, grid, st);
 }
 
 // Multi-token query (chunk of new tokens per sequence, causal within it).
-template <int KT>
+template <int KT, bool MOD = false>
 cudaError_t launch_prefill_dt(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int DH, int P,
                               dim3 grid, cudaStream_t st) {
     if (DH == 128)
-        return P == 16 ? launch_mma_inst<KT, KT, 128, 16, false, true>(p, tk, tv, grid, st)
-                       : launch_mma_inst<KT, KT, 128, 32, false, true>(p, tk, tv, grid, st);
-    return P == 16 ? launch_mma_inst<KT, KT, 64, 16, false, true>(p, tk, tv, grid, st)
-                   : launch_mma_inst<KT, KT, 64, 32, false, true>(p, tk, tv, grid, st);
+        return P == 16 ? launch_mma_inst<KT, KT, 128, 16, false, true, MOD>(p, tk, tv, grid, st)
+                       : launch_mma_inst<KT, KT, 128, 32, false, true, MOD>(p, tk, tv, grid, st);
+    return P == 16 ? launch_mma_inst<KT, KT, 64, 16, false, true, MOD>(p, tk, tv, grid, st)
+                   : launch_mma_inst<KT, KT, 64, 32, false, true, MOD>(p, tk, tv, grid, st);
 }
 
 // Defined in decode_mma_bf16.cu / decode_mma_f16.cu / decode_mma_fp8.cu.
@@ -156,5 +157,15 @@ cudaError_t launch_tc_fp8(const DecodeParams& p, const CUtensorMap& tk, const CU
 // E4M3 K/V with q of type q_dtype (bf16 or fp16).
 cudaError_t launch_mma_fp8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int q_dtype, int DH,
                            int P, dim3 grid, cudaStream_t st);
+// int8 K/V with scales per token (decode_mma_int8.cu), q of type q_dtype (bf16 or fp16).
+cudaError_t launch_mma_int8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int q_dtype, int DH,
+                            int P, dim3 grid, cudaStream_t st);
+// Modified scores and masks over 16-bit K/V (decode_mma_mod.cu, prefill_mma_mod.cu, prefill_tc_mod.cu).
+cudaError_t launch_mma_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH, int P,
+                           dim3 grid, cudaStream_t st);
+cudaError_t launch_prefill_tc_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int P,
+                                  dim3 grid, cudaStream_t st);
+cudaError_t launch_prefill_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH,
+                               int P, dim3 grid, cudaStream_t st);
 
 }  // namespace kvp

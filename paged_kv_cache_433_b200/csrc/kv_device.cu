@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "combine_kernel.cuh"
@@ -14,6 +15,7 @@
 #include "fp8.cuh"
 #include "kvpaged.h"
 #include "plan_kernel.cuh"
+#include "score_mod.cuh"
 
 namespace kvp {
 
@@ -187,6 +189,10 @@ int keep_shared_carveout() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<128, kCombineWarps>, a, c);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, 1>, a, c);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, kCombineWarps>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<128, 1, true>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<128, kCombineWarps, true>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, 1, true>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, kCombineWarps, true>, a, c);
     if (e != cudaSuccess) return -1;
     done.fetch_or(bit, std::memory_order_acq_rel);
     return 0;
@@ -270,7 +276,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 bool make_pool_map(CUtensorMap* m, const void* base, int32_t dtype, int64_t rows, int32_t Dh, int32_t P) {
     auto enc = tensor_map_encoder();
     if (!enc || rows >= (1LL << 32)) return false;
-    const int eb = elem_bytes(dtype);
+    const int eb = dtype == KV_DTYPE_INT8 ? 1 : elem_bytes(dtype);
     const int row_bytes = Dh * eb;
     const int box_bytes = row_bytes < 128 ? row_bytes : 128;
     cuuint64_t gdim[2] = {static_cast<cuuint64_t>(Dh), static_cast<cuuint64_t>(rows)};
@@ -287,10 +293,11 @@ bool make_pool_map(CUtensorMap* m, const void* base, int32_t dtype, int64_t rows
 }
 
 // Tensor cores for 16-bit K/V when the GQA group fits 4 slices of 16 rows.
-// E4M3 K/V exist only on the tensor-core kernel.
+// E4M3 and int8 K/V exist only on the tensor-core kernel.
 bool use_mma(int32_t dtype, int32_t g) {
     const int kind = g_kernel_kind.load(std::memory_order_relaxed);
     if (dtype == KV_DTYPE_F32) return false;
+    if (dtype == KV_DTYPE_INT8) return g <= 64;
     if (kind == KV_DECODE_KERNEL_SIMT && dtype != KV_DTYPE_FP8_E4M3) return false;
     return g <= 64;
 }
@@ -399,13 +406,49 @@ bool make_q_map(CUtensorMap* m, const void* q, int32_t dtype, int64_t rows, int3
     return r == CUDA_SUCCESS;
 }
 
-int check_shape(int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t dtype) {
+// What the int8 cache and the modified scores and masks add to a decode launch (the E4M3 pools of
+// paged_decode_attention_fp8 have per-head scales of their own).
+struct DecodeExtra {
+    bool int8 = false;                 // int8 pools (dtype KV_DTYPE_INT8) with kv_scales
+    const float* kv_scales = nullptr;
+    bool mod = false;                  // modified scores and masks, 16-bit pools
+    float softcap = 0.f;
+    const float* alibi_slopes = nullptr;
+    int32_t window = 0;
+    const int32_t* key_start = nullptr;
+};
+
+int check_mod(float softcap, int32_t window) {
+    return softcap >= 0.f && softcap < 3.0e38f && window >= 0 ? KV_OK : KV_ERR_ARG;  // a NaN fails the comparison
+}
+
+void set_mod(DecodeParams& p, float scale, float softcap, const float* alibi_slopes, int32_t window,
+             const int32_t* key_start) {
+    p.cap_in = softcap > 0.f ? scale / softcap : 0.f;
+    p.cap_out = softcap * kLog2e;
+    // the polynomial of the capped score in the square of the product q . k (score_mod.cuh); where its
+    // coefficients leave fp32's range every score takes the exponential form
+    const double u = p.cap_in, o = static_cast<double>(scale) * 1.4426950408889634;
+    double f = o, top = 0.;
+    for (int i = 0; i < kCapTerms; ++i, f *= u * u) {
+        p.cap_coef[i] = static_cast<float>(kTanhPoly[i] * f);
+        top = std::max(top, std::abs(kTanhPoly[i] * f));
+    }
+    p.cap_small = u != 0. && top < 1e30 && kTanhSmall / std::abs(u) < 1e15 ? static_cast<float>(kTanhSmall / std::abs(u)) : -1.f;
+    p.alibi_slopes = alibi_slopes;
+    p.window = window;
+    p.key_start = key_start;
+}
+
+int check_shape(int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t dtype, bool mma_only = false) {
     if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0) return KV_ERR_ARG;
-    if (elem_bytes(dtype) == 0) return KV_ERR_ARG;
+    if (dtype != KV_DTYPE_INT8 && elem_bytes(dtype) == 0) return KV_ERR_ARG;
     if (Dh != 64 && Dh != 128) return KV_ERR_UNSUPPORTED;
     if (page_size != 16 && page_size != 32) return KV_ERR_UNSUPPORTED;
     int a, b, c, d;
-    if (dtype == KV_DTYPE_FP8_E4M3) return use_mma(dtype, H_q / H_kv) ? KV_OK : KV_ERR_UNSUPPORTED;
+    if (mma_only) return H_q / H_kv <= 64 ? KV_OK : KV_ERR_UNSUPPORTED;
+    if (dtype == KV_DTYPE_FP8_E4M3 || dtype == KV_DTYPE_INT8)
+        return use_mma(dtype, H_q / H_kv) ? KV_OK : KV_ERR_UNSUPPORTED;
     if (!use_mma(dtype, H_q / H_kv) && !plan_group(H_q / H_kv, &a, &b, &c, &d)) return KV_ERR_UNSUPPORTED;
     return KV_OK;
 }
@@ -531,11 +574,16 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
                 int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t dtype,
                 int32_t num_splits, void* workspace, size_t ws_bytes, int* err_flag, void* stream,
                 int32_t q_dtype = -1, const float* k_scale = nullptr, const float* v_scale = nullptr,
-                const float* cos_sin = nullptr, int32_t max_pos = 0, int32_t rope_style = 0) {
-    int rc = check_shape(H_q, H_kv, Dh, page_size, dtype);
+                const float* cos_sin = nullptr, int32_t max_pos = 0, int32_t rope_style = 0,
+                const DecodeExtra& ex = DecodeExtra()) {
+    if (dtype == KV_DTYPE_INT8 && !ex.int8) return KV_ERR_ARG;  // only through paged_decode_attention_int8
+    int rc = check_shape(H_q, H_kv, Dh, page_size, dtype, ex.mod);
     if (rc != KV_OK) return rc;
     if (q_dtype < 0) q_dtype = dtype;
-    if (dtype == KV_DTYPE_FP8_E4M3) {
+    if (dtype == KV_DTYPE_INT8) {
+        if (q_dtype != KV_DTYPE_BF16 && q_dtype != KV_DTYPE_F16) return KV_ERR_ARG;
+        if (B > 0 && (!ex.kv_scales || !aligned16(ex.kv_scales))) return KV_ERR_ARG;
+    } else if (dtype == KV_DTYPE_FP8_E4M3) {
         if (q_dtype != KV_DTYPE_BF16 && q_dtype != KV_DTYPE_F16) return KV_ERR_ARG;
         if (k_new != nullptr || v_new != nullptr) return KV_ERR_UNSUPPORTED;  // quantising append: kv_append_fp8
         if (B > 0 && (!k_scale || !v_scale)) return KV_ERR_ARG;
@@ -549,8 +597,9 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages)) return KV_ERR_ARG;
     const int32_t g = H_q / H_kv;
     // TMA row coordinates are int32: very large pools stay on the CUDA-core kernel.
-    const bool mma = use_mma(dtype, g) && static_cast<int64_t>(num_pages) * H_kv * page_size < (1LL << 31);
-    if (dtype == KV_DTYPE_FP8_E4M3 && !mma) return KV_ERR_UNSUPPORTED;
+    const bool mma = (ex.mod ? g <= 64 : use_mma(dtype, g)) &&
+                     static_cast<int64_t>(num_pages) * H_kv * page_size < (1LL << 31);
+    if ((dtype == KV_DTYPE_FP8_E4M3 || dtype == KV_DTYPE_INT8 || ex.mod) && !mma) return KV_ERR_UNSUPPORTED;
     int GW = 0, HS, NW, WP;
     if (mma) {
         HS = (g + 15) / 16;
@@ -560,9 +609,23 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         plan_group(g, &GW, &HS, &NW, &WP);
     }
     int32_t S, C;
-    rc = resolve_splits(B, H_kv, max_blocks, num_splits, &S, &C, elem_bytes(dtype));
+    const int kv_bytes = dtype == KV_DTYPE_INT8 ? 1 : elem_bytes(dtype);
+    rc = resolve_splits(B, H_kv, max_blocks, num_splits, &S, &C, kv_bytes);
     if (rc != KV_OK) return rc;
-    const bool tc = mma && tc_ok(dtype, g, Dh, cos_sin != nullptr, B, H_kv, num_splits);
+    if (ex.mod && ex.window > 0) {
+        // a window touches at most nb pages of any row: split those (never more splits than without a window, so
+        // that the workspace of the same arguments holds their partials)
+        const int64_t nb64 = (static_cast<int64_t>(ex.window) + page_size - 2) / page_size + 1;
+        if (nb64 < max_blocks) {
+            const int32_t nb = static_cast<int32_t>(nb64), S_all = S;
+            rc = resolve_splits(B, H_kv, nb, num_splits, &S, &C, kv_bytes);
+            if (rc != KV_OK) return rc;
+            C = (nb + std::min(S, S_all) - 1) / std::min(S, S_all);
+            S = (nb + C - 1) / C;
+        }
+    }
+    const bool new_op = ex.mod || dtype == KV_DTYPE_INT8;  // on the warp-MMA kernel only
+    const bool tc = mma && !new_op && tc_ok(dtype, g, Dh, cos_sin != nullptr, B, H_kv, num_splits);
     const bool planned = tc ? planned_tc(B, num_splits) : planned_ok(mma, B, H_q, H_kv, num_splits);
 
     DecodeParams p{};
@@ -591,6 +654,8 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
     p.cos_sin = cos_sin;
     p.max_pos = max_pos;
     p.rope_style = rope_style;
+    p.kv_scales = ex.kv_scales;
+    set_mod(p, scale, ex.softcap, ex.alibi_slopes, ex.window, ex.key_start);
     if (cos_sin != nullptr && !mma) return KV_ERR_UNSUPPORTED;  // the fused rotation lives in the tensor-core kernel
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     dim3 grid(static_cast<unsigned>(S), static_cast<unsigned>(H_kv), static_cast<unsigned>(B));
@@ -635,14 +700,14 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         p.part_ml = reinterpret_cast<float2*>(w + L.ml_off);
         p.num_splits = 0;
         // chunk floor: a chunk's partial (g x (Dh + 2) fp32) at most ~6 % of its K/V bytes
-        const int64_t chunk_bytes_per_page = 2LL * page_size * Dh * elem_bytes(dtype);
+        const int64_t chunk_bytes_per_page = 2LL * page_size * Dh * kv_bytes;
         const int64_t partial_bytes = static_cast<int64_t>(H_q / H_kv) * (Dh + 2) * 4;
         const int32_t c_floor = static_cast<int32_t>(std::max<int64_t>(8, (16 * partial_bytes + chunk_bytes_per_page - 1) /
                                                                                 chunk_bytes_per_page));
         // resident CTAs of the warp-MMA kernel: two per SM
         const int32_t slots = static_cast<int32_t>(2 * sms_all);
         e = launch_pdl(paged_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, seq_lens, B, H_kv, page_size, max_blocks,
-                       slots, static_cast<int32_t>(pgrid), c_floor, plan, items, err_flag);
+                       slots, static_cast<int32_t>(pgrid), c_floor, plan, items, p.window, p.key_start, err_flag);
         if (e != cudaSuccess) return KV_ERR_CUDA;
         grid = dim3(static_cast<unsigned>(pgrid), 1, 1);
     } else if (S > 1) {
@@ -673,7 +738,9 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) ||
             !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
             return KV_ERR_CUDA;
-        e = dtype == KV_DTYPE_BF16   ? launch_mma_bf16(p, tk, tv, Dh, page_size, grid, st)
+        e = ex.mod                   ? launch_mma_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
+            : dtype == KV_DTYPE_INT8 ? launch_mma_int8(p, tk, tv, q_dtype, Dh, page_size, grid, st)
+            : dtype == KV_DTYPE_BF16 ? launch_mma_bf16(p, tk, tv, Dh, page_size, grid, st)
             : dtype == KV_DTYPE_F16 ? launch_mma_f16(p, tk, tv, Dh, page_size, grid, st)
                                     : launch_mma_fp8(p, tk, tv, q_dtype, Dh, page_size, grid, st);
     } else {
@@ -703,16 +770,19 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         const dim3 threads(32 * kCombineWarps);
         const float2* ml = p.part_ml;
         const float* pu = p.part_u;
-        if (Dh == 128)
-            e = narrow ? launch_pdl(paged_combine_kernel<128, 1>, blocks, threads, 0, st, out, pu, ml, seq_lens, B, H_q,
-                                    S, C, page_size, max_blocks, plan, H_kv)
-                       : launch_pdl(paged_combine_kernel<128, kCombineWarps>, blocks, threads, 0, st, out, pu, ml,
-                                    seq_lens, B, H_q, S, C, page_size, max_blocks, plan, H_kv);
+        auto combine = [&](auto kernel) {
+            return launch_pdl(kernel, blocks, threads, 0, st, out, pu, ml, seq_lens, B, H_q, S, C, page_size, max_blocks,
+                              plan, H_kv, p.window, p.key_start);
+        };
+        if (new_op && Dh == 128)
+            e = narrow ? combine(paged_combine_kernel<128, 1, true>)
+                       : combine(paged_combine_kernel<128, kCombineWarps, true>);
+        else if (new_op)
+            e = narrow ? combine(paged_combine_kernel<64, 1, true>) : combine(paged_combine_kernel<64, kCombineWarps, true>);
+        else if (Dh == 128)
+            e = narrow ? combine(paged_combine_kernel<128, 1>) : combine(paged_combine_kernel<128, kCombineWarps>);
         else
-            e = narrow ? launch_pdl(paged_combine_kernel<64, 1>, blocks, threads, 0, st, out, pu, ml, seq_lens, B, H_q, S,
-                                    C, page_size, max_blocks, plan, H_kv)
-                       : launch_pdl(paged_combine_kernel<64, kCombineWarps>, blocks, threads, 0, st, out, pu, ml,
-                                    seq_lens, B, H_q, S, C, page_size, max_blocks, plan, H_kv);
+            e = narrow ? combine(paged_combine_kernel<64, 1>) : combine(paged_combine_kernel<64, kCombineWarps>);
         if (e != cudaSuccess) return KV_ERR_CUDA;
     }
     return KV_OK;
@@ -752,6 +822,39 @@ int paged_decode_attention_fp8(float* out, const void* q, int32_t q_dtype, const
                        stream, q_dtype, k_scale, v_scale);
 }
 
+int paged_decode_attention_int8(float* out, const void* q, int32_t q_dtype, const void* k_pages, const void* v_pages,
+                                const float* kv_scales, const int32_t* block_tables, int32_t max_blocks,
+                                const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
+                                int32_t page_size, int32_t num_pages, float scale, int32_t num_splits, void* workspace,
+                                size_t ws_bytes, int* err_flag, void* stream) {
+    DecodeExtra ex;
+    ex.int8 = true;
+    ex.kv_scales = kv_scales;
+    return decode_impl(out, q, nullptr, nullptr, k_pages, v_pages, block_tables, max_blocks, seq_lens, B, H_q, H_kv, Dh,
+                       page_size, num_pages, scale, KV_DTYPE_INT8, num_splits, workspace, ws_bytes, err_flag, stream,
+                       q_dtype, nullptr, nullptr, nullptr, 0, 0, ex);
+}
+
+int paged_decode_attention_mod(float* out, const void* q, const void* k_pages, const void* v_pages,
+                               const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens, int32_t B,
+                               int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, float scale,
+                               int32_t dtype, float softcap, const float* alibi_slopes, int32_t window,
+                               const int32_t* key_start, int32_t num_splits, void* workspace, size_t ws_bytes,
+                               int* err_flag, void* stream) {
+    if (dtype != KV_DTYPE_BF16 && dtype != KV_DTYPE_F16) return dtype == KV_DTYPE_F32 ? KV_ERR_UNSUPPORTED : KV_ERR_ARG;
+    const int rc = check_mod(softcap, window);
+    if (rc != KV_OK) return rc;
+    DecodeExtra ex;
+    ex.mod = true;
+    ex.softcap = softcap;
+    ex.alibi_slopes = alibi_slopes;
+    ex.window = window;
+    ex.key_start = key_start;
+    return decode_impl(out, q, nullptr, nullptr, k_pages, v_pages, block_tables, max_blocks, seq_lens, B, H_q, H_kv, Dh,
+                       page_size, num_pages, scale, dtype, num_splits, workspace, ws_bytes, err_flag, stream, dtype,
+                       nullptr, nullptr, nullptr, 0, 0, ex);
+}
+
 int paged_decode_attention_rope_append(float* out, const void* q, const void* k_new, const void* v_new,
                                        void* k_pages, void* v_pages, const int32_t* block_tables, int32_t max_blocks,
                                        const int32_t* seq_lens, const float* cos_sin, int32_t max_pos,
@@ -768,11 +871,23 @@ int paged_decode_attention_rope_append(float* out, const void* q, const void* k_
                        nullptr, nullptr, cos_sin, max_pos, rope_style);
 }
 
-int paged_prefill_attention(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
-                            const void* k_pages, const void* v_pages, const int32_t* block_tables, int32_t max_blocks,
-                            const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
-                            int32_t page_size, int32_t num_pages, float scale, int32_t dtype, int* err_flag,
-                            void* stream) {
+}  // extern "C"
+
+namespace kvp {
+namespace {
+
+// mod: the modified scores and masks of paged_prefill_attention_mod (nullptr: plain causal attention).
+struct PrefillMod {
+    float softcap;
+    const float* alibi_slopes;
+    int32_t window;
+    const int32_t *key_start, *prefix_lens;
+};
+
+int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_q_len, const void* k_pages,
+                 const void* v_pages, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens, int32_t B,
+                 int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t dtype,
+                 int* err_flag, void* stream, const PrefillMod* mod) {
     if (dtype != KV_DTYPE_BF16 && dtype != KV_DTYPE_F16) return dtype == KV_DTYPE_F32 ? KV_ERR_UNSUPPORTED : KV_ERR_ARG;
     if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0) return KV_ERR_ARG;
     if (Dh != 64 && Dh != 128) return KV_ERR_UNSUPPORTED;
@@ -811,6 +926,10 @@ int paged_prefill_attention(float* out, const void* q, const int32_t* q_start, i
     p.scale_log2 = scale * kLog2e;
     p.q_start = q_start;
     p.q_tile = q_tile;
+    if (mod) {
+        set_mod(p, scale, mod->softcap, mod->alibi_slopes, mod->window, mod->key_start);
+        p.prefix_lens = mod->prefix_lens;
+    }
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;
     if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) || !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
@@ -818,10 +937,39 @@ int paged_prefill_attention(float* out, const void* q, const int32_t* q_start, i
     const dim3 grid(static_cast<unsigned>((max_q_len + q_tile - 1) / q_tile), static_cast<unsigned>(H_kv),
                     static_cast<unsigned>(B));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = tc                       ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
+    const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
+                          : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, grid, st)
+                          : tc                     ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
                           : dtype == KV_DTYPE_BF16 ? launch_prefill_bf16(p, tk, tv, Dh, page_size, grid, st)
                                                    : launch_prefill_f16(p, tk, tv, Dh, page_size, grid, st);
     return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kvp
+
+extern "C" {
+
+int paged_prefill_attention(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
+                            const void* k_pages, const void* v_pages, const int32_t* block_tables, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
+                            int32_t page_size, int32_t num_pages, float scale, int32_t dtype, int* err_flag,
+                            void* stream) {
+    return prefill_impl(out, q, q_start, max_q_len, k_pages, v_pages, block_tables, max_blocks, seq_lens, B, H_q, H_kv,
+                        Dh, page_size, num_pages, scale, dtype, err_flag, stream, nullptr);
+}
+
+int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
+                                const void* k_pages, const void* v_pages, const int32_t* block_tables,
+                                int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
+                                int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t dtype,
+                                float softcap, const float* alibi_slopes, int32_t window, const int32_t* key_start,
+                                const int32_t* prefix_lens, int* err_flag, void* stream) {
+    const int rc = check_mod(softcap, window);
+    if (rc != KV_OK) return rc;
+    const PrefillMod mod{softcap, alibi_slopes, window, key_start, prefix_lens};
+    return prefill_impl(out, q, q_start, max_q_len, k_pages, v_pages, block_tables, max_blocks, seq_lens, B, H_q, H_kv,
+                        Dh, page_size, num_pages, scale, dtype, err_flag, stream, &mod);
 }
 
 int kv_append_fp8(void* k_pages, void* v_pages, const void* k_new, const void* v_new, int32_t src_dtype,

@@ -6,6 +6,14 @@
 
 namespace kvp {
 
+// First key that a query at position pos may see: within the window (0: none)
+// and not before key_start[row] (nullable; negative entries count as 0).
+__device__ __forceinline__ int first_visible_key(int pos, int window, const int32_t* key_start, int row) {
+    int lo = window > 0 ? max(0, pos - window + 1) : 0;
+    if (key_start != nullptr) lo = max(lo, __ldcg(key_start + row));
+    return lo;
+}
+
 constexpr int kPlanHdr = 4;  // header words before the per-sequence arrays
 
 // Balanced plan (paged_plan_stream_kernel): [0] kPlanStream, [1] G | v << 16,

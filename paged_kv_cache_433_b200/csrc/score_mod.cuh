@@ -1,0 +1,185 @@
+// Modified attention scores and masks, shared by the decode and prefill
+// kernels: for query row i at position pos and key t,
+//   s = scale * (q . k);  s = c * tanh(s / c) (if a cap c is set);
+//   s -= slope_h * |pos - t| (if slopes are given),
+// and the row sees the keys t in [lo, hi):
+//   lo = max(0, key_start[i], pos - window + 1), hi = max(pos + 1, prefix_b),
+// prefix_b = min(prefix_lens[b], seq_lens[b]). A row with lo >= hi sees none.
+// Scores come out in log2 units (times log2 e).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "decode_kernel.cuh"
+#include "plan_layout.cuh"
+
+namespace kvp {
+
+// First key that the query in row `row` (of key_start) at position pos may see.
+__device__ __forceinline__ int first_key(const DecodeParams& p, int row, int pos) {
+    return first_visible_key(pos, p.window, p.key_start, row);
+}
+
+// Keys of a tile of nt query rows (chunk tokens) at positions pos0 ..: some row sees keys in [begin, end) only;
+// every row sees all keys in [all0, all1). Called by whole warps.
+struct TileKeys {
+    int begin, end, all0, all1;
+};
+__device__ __forceinline__ TileKeys tile_keys(const DecodeParams& p, int row0, int pos0, int nt, int prefix, int lane) {
+    TileKeys k;
+    k.end = max(pos0 + nt, prefix);
+    k.all1 = max(pos0 + 1, prefix);
+    int lo_min = first_visible_key(pos0, p.window, nullptr, 0);
+    int lo_max = first_visible_key(pos0 + nt - 1, p.window, nullptr, 0);
+    if (p.key_start != nullptr) {
+        lo_min = 0x7fffffff;
+        lo_max = 0;
+        for (int t = lane; t < nt; t += 32) {
+            const int lo = first_key(p, row0 + t, pos0 + t);
+            lo_min = min(lo_min, lo);
+            lo_max = max(lo_max, lo);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+            lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+        }
+    }
+    k.begin = lo_min;
+    k.all0 = lo_max;
+    return k;
+}
+
+// tanh(u) = 1 - 2 / (1 + e^2u): absolute error about 1e-7 for every u (+-inf give +-1).
+__device__ __forceinline__ float tanh_any(float u) {
+    return 1.f - 2.f * __frcp_rn(1.f + exp2f(u * 2.885390081777927f));
+}
+
+// Where |u| <= kTanhSmall: tanh(u) = u * P(u^2), P of degree 5 fitted to tanh(u) / u by least squares reweighted
+// towards equal relative errors (2.9e-8). No special-function unit, and relative instead of absolute accuracy:
+// scores that are small beside the cap, the usual case, keep all their bits. With u = x * scale / c for a product
+// x = q . k, the capped score in log2 units is x times a polynomial in x^2 whose coefficients the host scales by
+// the powers of (scale / c)^2 (p.cap_coef), valid for |x| <= p.cap_small.
+constexpr int kCapTerms = 6;
+constexpr double kTanhSmall = 0.75;
+constexpr double kTanhPoly[kCapTerms] = {0.999999971, -0.333329589, 0.13325406, -0.0533444284, 0.0195829047, -0.00471625478};
+__device__ __forceinline__ float2 cap_small2(const DecodeParams& p, float2 x) {
+    const float2 z = fmul2(x, x);
+    float2 r = make_float2(p.cap_coef[5], p.cap_coef[5]);
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) r = ffma2(z, r, make_float2(p.cap_coef[i], p.cap_coef[i]));
+    return fmul2(x, r);
+}
+
+// Products q . k of one warp's MMA tiles -> modified scores. sc[n][e]: row h = e / 2, token n * 8 + (e & 1) of the
+// stage counted from the lane's first; dist0 / dist1: position minus that first token for rows 0 / 1. LO: only
+// row 0 is real.
+template <int NT, bool LO>
+__device__ __forceinline__ void modify_scores(const DecodeParams& p, float (&sc)[NT][4], const float (&slope)[2],
+                                              int dist0, int dist1) {
+    constexpr int E = LO ? 2 : 4;
+    if (p.cap_out != 0.f) {
+        float big = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(sc[n][e]));
+        if (__any_sync(0xffffffffu, big > p.cap_small)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < E; ++e) sc[n][e] = tanh_any(sc[n][e] * p.cap_in) * p.cap_out;
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 t = cap_small2(p, make_float2(sc[n][e], sc[n][e + 1]));
+                    sc[n][e] = t.x;
+                    sc[n][e + 1] = t.y;
+                }
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < E; ++e) sc[n][e] *= p.scale_log2;
+    }
+    if (p.alibi_slopes != nullptr) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = static_cast<float>((e >= 2 ? dist1 : dist0) - (n * 8 + (e & 1)));
+                sc[n][e] -= slope[e >> 1] * fabsf(d);
+            }
+    }
+}
+
+// The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key.
+template <int N>
+__device__ __forceinline__ void modify_row(const DecodeParams& p, float (&s)[N], float slope, int dist0) {
+    if (p.cap_out != 0.f) {
+        float big = 0.f;
+#pragma unroll
+        for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(s[c]));
+        if (__any_sync(0xffffffffu, big > p.cap_small)) {
+#pragma unroll
+            for (int c = 0; c < N; ++c) s[c] = tanh_any(s[c] * p.cap_in) * p.cap_out;
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+                const float2 t = cap_small2(p, make_float2(s[c], s[c + 1]));
+                s[c] = t.x;
+                s[c + 1] = t.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] *= p.scale_log2;
+    }
+    if (p.alibi_slopes != nullptr) {
+        const float d = static_cast<float>(dist0);
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] -= slope * fabsf(d - static_cast<float>(c));
+    }
+}
+
+// ---- 16-bit values with an all-ones exponent (NaN, +-inf) -----------------
+// The halves of w that are not finite, with 0 in the place of finite ones.
+template <bool IS_BF16>
+__device__ __forceinline__ uint32_t nonfinite16(uint32_t w) {
+    constexpr uint32_t m = IS_BF16 ? 0x7f807f80u : 0x7c007c00u;
+    return w & __vcmpeq2(w & m, m);
+}
+template <bool IS_BF16>
+__device__ __forceinline__ bool has_nonfinite16(const uint4& v) {
+    return (nonfinite16<IS_BF16>(v.x) | nonfinite16<IS_BF16>(v.y) | nonfinite16<IS_BF16>(v.z) |
+            nonfinite16<IS_BF16>(v.w)) != 0;
+}
+template <bool IS_BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    if constexpr (IS_BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xffffu))),
+                           __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))));
+}
+
+// Sum of the NaN and infinite elements of dim d of V over keys lo .. hi - 1 of sequence b (pages outside the pool
+// left out): what an attention sum over those keys is once it holds one.
+template <bool IS_BF16>
+__device__ __noinline__ float sum_nonfinite(const DecodeParams& p, int b, int kvh, int P, int DH, int d, int lo, int hi) {
+    float acc = 0.f;
+    for (int t = lo; t < hi; ++t) {
+        const int pg = p.block_tables[(int64_t)b * p.max_blocks + t / P];
+        if (pg < 0 || pg >= p.num_pages) continue;
+        const uint32_t v = static_cast<const uint16_t*>(p.v_pages)[(((int64_t)pg * p.H_kv + kvh) * P + t % P) * DH + d];
+        acc += unpack16<IS_BF16>(nonfinite16<IS_BF16>(v)).x;
+    }
+    return acc;
+}
+
+}  // namespace kvp

@@ -86,6 +86,22 @@ SIGNATURES = [
       _i32, _vp, _sz, _vp, _vp]),
     ("paged_prefill_attention", ctypes.c_int,
      [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp]),
+    ("kv_norm_rope_append", ctypes.c_int,
+     [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+      _i32, _i32, _i32, _i32, _vp, _vp]),
+    ("kv_append_int8", ctypes.c_int,
+     [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    ("kv_dequant_pages_int8", ctypes.c_int,
+     [_vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    ("kv_copy_pages_int8", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    ("paged_decode_attention_int8", ctypes.c_int,
+     [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp]),
+    ("paged_decode_attention_mod", ctypes.c_int,
+     [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32, _vp, _i32,
+      _vp, _sz, _vp, _vp]),
+    ("paged_prefill_attention_mod", ctypes.c_int,
+     [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32,
+      _vp, _vp, _vp, _vp]),
     ("paged_decode_set_kernel", ctypes.c_int, [_i32]),
     ("paged_decode_num_splits", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _pi32]),
     ("paged_decode_launch_info", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _pi32, _pi32]),
@@ -426,6 +442,211 @@ def paged_prefill_attention(out, q, q_start, max_q_len: int, k_pages, v_pages, b
         B, H_q, H_kv, Dh, P, num_pages, float(scale), _torch_dtype_code(k_pages), _dev(err_flag, "err_flag", torch.int32),
         _stream(stream))
     _check("paged_prefill_attention", rc)
+
+
+# ---- per-head norm + rotation + append, int8 cache, modified scores and masks
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _here(t, name: str, shape=None, dtype=None):
+    """Pointer of a contiguous tensor on the current device, of this shape and dtype (None passes through)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    import torch
+
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _token_rows(t, name: str, shape, dtype):
+    """(pointer, elements from token to token) of a [B, H, Dh] tensor whose heads are contiguous within a token."""
+    import torch
+
+    B, H, Dh = shape
+    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(), f"{name} must be on the current CUDA device")
+    _need(t.dtype == dtype, f"{name} must be {dtype}")
+    _need(tuple(t.shape) == tuple(shape), f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need((Dh == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == Dh), f"the heads of a token of {name} must be contiguous")
+    return t.data_ptr(), (t.stride(0) if B > 1 else H * Dh)
+
+
+def _flag(err_flag):
+    import torch
+
+    if err_flag is None:
+        return None
+    _need(err_flag.numel() >= 1, "err_flag is empty")
+    return _here(err_flag, "err_flag", dtype=torch.int32)
+
+
+def _scratch(workspace):
+    return (None, 0) if workspace is None else (_here(workspace, "workspace"), workspace.numel() * workspace.element_size())
+
+
+def _pools(k_pages, v_pages, dtypes):
+    """Shape (num_pages, H_kv, P, Dh) and pointers of a pool pair whose dtype is one of `dtypes`."""
+    _need(k_pages.dim() == 4 and k_pages.dtype in dtypes, f"the pools must be [num_pages, H_kv, P, Dh] of {dtypes}")
+    return k_pages.shape, _here(k_pages, "k_pages"), _here(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
+
+
+def _ids(t, name: str, n: int, dtype):
+    return _here(t, name, (n,), dtype) if n else None
+
+
+def kv_norm_rope_append(k_pages, v_pages, k_new, v_new, slot_mapping, positions, cos_sin, k_weight, eps: float,
+                        page_size: int, style: str = "half", q=None, q_out=None, q_weight=None, k_out=None,
+                        err_flag=None, stream=None) -> None:
+    """RMS norm of every q and k head (weights fp32 [Dh] or None), rotation by `positions`, append -- one pass.
+
+    q [B, H_q, Dh], k/v_new [B, H_kv, Dh]: the heads of a token contiguous, tokens any stride apart (slices of one
+    projection's output); q_out, k_out contiguous. k/v_pages, v_new and slot_mapping may be None together when k_out
+    is given (a quantising append writes the cache then). Other arguments as kv_rope_append."""
+    import torch
+
+    B, H_kv, Dh = k_new.shape
+    dt = k_new.dtype
+    num_pages, kp, vp, vptr, vs, slots = 0, None, None, None, 0, None
+    if k_pages is not None:
+        (num_pages, Hp, P, Dp), kp, vp = _pools(k_pages, v_pages, (dt,))
+        _need((Hp, P, Dp) == (H_kv, page_size, Dh), "the pools must be [num_pages, H_kv, page_size, Dh]")
+        vptr, vs = _token_rows(v_new, "v_new", (B, H_kv, Dh), dt)
+        slots = _ids(slot_mapping, "slot_mapping", B, torch.int64)
+    else:
+        _need(v_pages is None and v_new is None and slot_mapping is None, "v_pages, v_new and slot_mapping need k_pages")
+    kptr, ks = _token_rows(k_new, "k_new", (B, H_kv, Dh), dt)
+    H_q, qptr, qs = 0, None, 0
+    if q is not None:
+        H_q = q.shape[1]
+        qptr, qs = _token_rows(q, "q", (B, H_q, Dh), dt)
+    _need((q is None) == (q_out is None), "q and q_out go together")
+    _need(cos_sin.dim() == 2 and cos_sin.shape[1] == Dh, "cos_sin must be [max_pos, Dh]")
+    rc = lib().kv_norm_rope_append(
+        kp, vp, _here(q_out, "q_out", (B, H_q, Dh), dt), _here(k_out, "k_out", (B, H_kv, Dh), dt), qptr, kptr, vptr, qs, ks,
+        vs, _here(q_weight, "q_weight", (Dh,), torch.float32), _here(k_weight, "k_weight", (Dh,), torch.float32), float(eps),
+        slots, _ids(positions, "positions", B, torch.int32), _here(cos_sin, "cos_sin", dtype=torch.float32),
+        cos_sin.shape[0], ROPE_STYLE[style], B, H_q, H_kv, Dh, page_size, num_pages, _torch_dtype_code(k_new),
+        _flag(err_flag), _stream(stream))
+    _check("kv_norm_rope_append", rc)
+
+
+def _int8_pools(k_pages, v_pages, kv_scales):
+    import torch
+
+    shape, kp, vp = _pools(k_pages, v_pages, (torch.int8,))
+    num_pages, H_kv, P, _ = shape
+    return shape, kp, vp, _here(kv_scales, "kv_scales", (num_pages, H_kv, 2, P), torch.float32)
+
+
+def kv_append_int8(k_pages, v_pages, kv_scales, k_new, v_new, slot_mapping, page_size: int, err_flag=None,
+                   stream=None) -> None:
+    """Quantise k/v_new [B, H_kv, Dh] (bf16/fp16/fp32; tokens any stride apart) row by row and append them into int8
+    pools [num_pages, H_kv, P, Dh] with their scales, fp32 [num_pages, H_kv, 2, P]."""
+    import torch
+
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    _need(P == page_size, "the pools' page size differs")
+    B = k_new.shape[0]
+    kptr, ks = _token_rows(k_new, "k_new", (B, H_kv, Dh), k_new.dtype)
+    vptr, vs = _token_rows(v_new, "v_new", (B, H_kv, Dh), k_new.dtype)
+    rc = lib().kv_append_int8(kp, vp, sc, kptr, vptr, ks, vs, _torch_dtype_code(k_new),
+                              _ids(slot_mapping, "slot_mapping", B, torch.int64), B, H_kv, Dh, P, num_pages,
+                              _flag(err_flag), _stream(stream))
+    _check("kv_append_int8", rc)
+
+
+def kv_dequant_pages_int8(k_out, v_out, k_pages, v_pages, kv_scales, src_pages, dst_pages, err_flag=None,
+                          stream=None) -> None:
+    """Pages src_pages[i] of the int8 pools -> pages dst_pages[i] of k/v_out [num_out_pages, H_kv, P, Dh]
+    (bf16/fp16/fp32); src/dst_pages int32 (device)."""
+    import torch
+
+    shape, kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    num_pages, H_kv, P, Dh = shape
+    oshape, ko, vo = _pools(k_out, v_out, (torch.bfloat16, torch.float16, torch.float32))
+    _need(oshape[1:] == shape[1:], "the output pools must have the int8 pools' heads, page size and Dh")
+    n = src_pages.numel()
+    rc = lib().kv_dequant_pages_int8(ko, vo, _torch_dtype_code(k_out), oshape[0], kp, vp, sc,
+                                     _ids(src_pages, "src_pages", n, torch.int32), _ids(dst_pages, "dst_pages", n, torch.int32),
+                                     n, H_kv, Dh, P, num_pages, _flag(err_flag), _stream(stream))
+    _check("kv_dequant_pages_int8", rc)
+
+
+def kv_copy_pages_int8(k_pages, v_pages, kv_scales, src_pages, dst_pages, err_flag=None, stream=None) -> None:
+    """kv_copy_pages of int8 pools: codes and scales of pages src_pages[i] -> dst_pages[i] (int32, device)."""
+    import torch
+
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    n = src_pages.numel()
+    rc = lib().kv_copy_pages_int8(kp, vp, sc, _ids(src_pages, "src_pages", n, torch.int32),
+                                  _ids(dst_pages, "dst_pages", n, torch.int32), n, H_kv, Dh, P, num_pages,
+                                  _flag(err_flag), _stream(stream))
+    _check("kv_copy_pages_int8", rc)
+
+
+def paged_decode_attention_int8(out, q, k_pages, v_pages, kv_scales, block_tables, seq_lens, scale: float,
+                                num_splits: int = 0, workspace=None, err_flag=None, stream=None) -> None:
+    """Decode over int8 pools [num_pages, H_kv, P, Dh] with scales [num_pages, H_kv, 2, P]; q bf16/fp16 [B, H_q, Dh];
+    other arguments as paged_decode_attention."""
+    import torch
+
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    B, H_q, _ = q.shape
+    ws, ws_bytes = _scratch(workspace)
+    rc = lib().paged_decode_attention_int8(
+        _here(out, "out", (B, H_q, Dh), torch.float32), _here(q, "q", (B, H_q, Dh)), _torch_dtype_code(q), kp, vp, sc,
+        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
+        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale), num_splits, ws,
+        ws_bytes, _flag(err_flag), _stream(stream))
+    _check("paged_decode_attention_int8", rc)
+
+
+def paged_decode_attention_mod(out, q, k_pages, v_pages, block_tables, seq_lens, scale: float, softcap: float = 0.0,
+                               alibi_slopes=None, window: int = 0, key_start=None, num_splits: int = 0, workspace=None,
+                               err_flag=None, stream=None) -> None:
+    """paged_decode_attention (bf16/fp16 pools) with capped scores (softcap > 0), a distance bias (alibi_slopes fp32
+    [H_q]), a sliding window (window > 0) and a first visible key per sequence (key_start int32 [B])."""
+    import torch
+
+    (num_pages, H_kv, P, Dh), kp, vp = _pools(k_pages, v_pages, (torch.bfloat16, torch.float16, torch.float32))
+    B, H_q, _ = q.shape
+    ws, ws_bytes = _scratch(workspace)
+    rc = lib().paged_decode_attention_mod(
+        _here(out, "out", (B, H_q, Dh), torch.float32), _here(q, "q", (B, H_q, Dh), k_pages.dtype), kp, vp,
+        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
+        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale),
+        _torch_dtype_code(k_pages), float(softcap), _here(alibi_slopes, "alibi_slopes", (H_q,), torch.float32), int(window),
+        _here(key_start, "key_start", (B,), torch.int32), num_splits, ws, ws_bytes, _flag(err_flag), _stream(stream))
+    _check("paged_decode_attention_mod", rc)
+
+
+def paged_prefill_attention_mod(out, q, q_start, max_q_len: int, k_pages, v_pages, block_tables, seq_lens, scale: float,
+                                softcap: float = 0.0, alibi_slopes=None, window: int = 0, key_start=None,
+                                prefix_lens=None, err_flag=None, stream=None) -> None:
+    """paged_prefill_attention with the score and mask options of paged_decode_attention_mod (key_start int32 [N], one
+    per row) and a bidirectional prefix per sequence (prefix_lens int32 [B])."""
+    import torch
+
+    (num_pages, H_kv, P, Dh), kp, vp = _pools(k_pages, v_pages, (torch.bfloat16, torch.float16, torch.float32))
+    N, H_q, _ = q.shape
+    B = seq_lens.shape[0]
+    rc = lib().paged_prefill_attention_mod(
+        _here(out, "out", (N, H_q, Dh), torch.float32), _here(q, "q", (N, H_q, Dh), k_pages.dtype),
+        _here(q_start, "q_start", (B + 1,), torch.int32), int(max_q_len), kp, vp,
+        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
+        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale),
+        _torch_dtype_code(k_pages), float(softcap), _here(alibi_slopes, "alibi_slopes", (H_q,), torch.float32), int(window),
+        _here(key_start, "key_start", (N,), torch.int32), _here(prefix_lens, "prefix_lens", (B,), torch.int32),
+        _flag(err_flag), _stream(stream))
+    _check("paged_prefill_attention_mod", rc)
 
 
 KV_DECODE_KERNEL_AUTO, KV_DECODE_KERNEL_SIMT, KV_DECODE_KERNEL_MMA, KV_DECODE_KERNEL_TCGEN05 = 0, 1, 2, 3
