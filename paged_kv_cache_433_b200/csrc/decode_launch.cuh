@@ -85,10 +85,9 @@ template <int KT, int QT, int DH, int P, bool LO, bool QM = false, bool MOD = fa
 cudaError_t launch_mma_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                             cudaStream_t st) {
     constexpr int NW = 4;
-    // one-byte pages of 16 tokens are half the bytes of a 16-bit page: two of them share a stage
-    constexpr bool k8 = KT == KV_DTYPE_FP8_E4M3 || KT == KV_DTYPE_INT8;
-    constexpr int PPS = (k8 && P == 16) ? 2 : 1;
-    using C = MmaCfg<DH, P, NW, k8 ? 1 : 2, PPS, KT == KV_DTYPE_INT8 ? 8 : 0>;
+    // E4M3 pages of 16 tokens are half the bytes of a 16-bit page: two of them share a stage
+    constexpr int PPS = (KT == KV_DTYPE_FP8_E4M3 && P == 16) ? 2 : 1;
+    using C = MmaCfg<DH, P, NW, KT == KV_DTYPE_FP8_E4M3 ? 1 : 2, PPS>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -107,21 +106,21 @@ cudaError_t launch_mma_inst(const DecodeParams& p, const CUtensorMap& tk, const 
 
 // Groups of at most 8 heads take the instance that carries the probability
 // residual in the MMA's padding rows.
-template <int KT, int QT, int DH, int P, bool MOD = false>
+template <int KT, int QT, int DH, int P>
 cudaError_t launch_mma_group(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                              cudaStream_t st) {
-    return p.g <= 8 ? launch_mma_inst<KT, QT, DH, P, true, false, MOD>(p, tk, tv, grid, st)
-                    : launch_mma_inst<KT, QT, DH, P, false, false, MOD>(p, tk, tv, grid, st);
+    return p.g <= 8 ? launch_mma_inst<KT, QT, DH, P, true>(p, tk, tv, grid, st)
+                    : launch_mma_inst<KT, QT, DH, P, false>(p, tk, tv, grid, st);
 }
 
-template <int KT, int QT, bool MOD = false>
+template <int KT, int QT>
 cudaError_t launch_mma_dt(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int DH, int P, dim3 grid,
                           cudaStream_t st) {
     if (DH == 128)
-        return P == 16 ? launch_mma_group<KT, QT, 128, 16, MOD>(p, tk, tv, grid, st)
-                       : launch_mma_group<KT, QT, 128, 32, MOD>(p, tk, tv, grid, st);
-    return P == 16 ? launch_mma_group<KT, QT, 64, 16, MOD>(p, tk, tv, grid, st)
-                   : launch_mma_group<KT, QT, 64, 32, MOD>(p, tk, tv, grid, st);
+        return P == 16 ? launch_mma_group<KT, QT, 128, 16>(p, tk, tv, grid, st)
+                       : launch_mma_group<KT, QT, 128, 32>(p, tk, tv, grid, st);
+    return P == 16 ? launch_mma_group<KT, QT, 64, 16>(p, tk, tv, grid, st)
+                   : launch_mma_group<KT, QT, 64, 32>(p, tk, tv, grid, st);
 }
 
 // Multi-token query (chunk of new tokens per sequence, causal within it).
@@ -157,12 +156,13 @@ cudaError_t launch_tc_fp8(const DecodeParams& p, const CUtensorMap& tk, const CU
 // E4M3 K/V with q of type q_dtype (bf16 or fp16).
 cudaError_t launch_mma_fp8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int q_dtype, int DH,
                            int P, dim3 grid, cudaStream_t st);
-// int8 K/V with scales per token (decode_mma_int8.cu), q of type q_dtype (bf16 or fp16).
-cudaError_t launch_mma_int8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int q_dtype, int DH,
-                            int P, dim3 grid, cudaStream_t st);
-// Modified scores and masks over 16-bit K/V (decode_mma_mod.cu, prefill_mma_mod.cu, prefill_tc_mod.cu).
-cudaError_t launch_mma_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH, int P,
-                           dim3 grid, cudaStream_t st);
+// Heads-as-columns kernel (decode_cols.cuh): int8 K/V with scales per token and q of type q_dtype (bf16 or fp16);
+// 16-bit K/V with modified scores and masks.
+cudaError_t launch_cols_int8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int q_dtype, int DH,
+                             int P, dim3 grid, cudaStream_t st);
+cudaError_t launch_cols_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH, int P,
+                            dim3 grid, cudaStream_t st);
+// Multi-token query with modified scores and masks (prefill_mma_mod.cu, prefill_tc_mod.cu).
 cudaError_t launch_prefill_tc_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int P,
                                   dim3 grid, cudaStream_t st);
 cudaError_t launch_prefill_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH,

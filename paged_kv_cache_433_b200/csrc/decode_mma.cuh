@@ -1,11 +1,10 @@
 // Paged decode attention on the tensor cores (bf16 / fp16 / E4M3 K/V), sm_100a.
-// One kernel template serves six uses: single-token decode (the default),
+// One kernel template serves five uses: single-token decode (the default),
 // E4M3 K/V (codes converted to f16 pairs in registers, two pages per stage),
-// int8 K/V (codes widened to f16 / bf16 pairs with integer operations, scales
-// per token fetched beside the pages), multi-token query (chunked prefill: MMA
-// rows are (token, head) pairs with a per-row causal limit), the fused rotate +
-// append + decode step, and modified scores and masks (tanh cap, distance bias,
-// sliding window, documents, bidirectional prefix) for decode and prefill.
+// multi-token query (chunked prefill: MMA rows are (token, head) pairs with a
+// per-row causal limit), the same with modified scores and masks (tanh cap,
+// distance bias, window, documents, bidirectional prefix), and the fused
+// rotate + append + decode step.
 //
 // Same contract and the same online (m, l, u) merge as decode_kernel.cuh
 // ("07｜KV Cache、FlashAttention与PagedAttention的内部过程", Q027; attention
@@ -101,9 +100,8 @@ __device__ __forceinline__ void append_new_token_rope(const DecodeParams& p, int
 // elements is loaded as boxes of at most 128 bytes (rows of 128 bytes use the
 // 128-byte swizzle, rows of 64 bytes -- E4M3 at Dh = 64 -- the 64-byte one).
 // PPS pages share one pipeline stage (tokens per stage TP = P * PPS): the
-// consumer then works on TP tokens per barrier round trip. SB: bytes of scales
-// per token (int8 K/V: 8, one fp32 for K and one for V).
-template <int DH, int P, int NW, int EB, int PPS, int SB = 0>
+// consumer then works on TP tokens per barrier round trip.
+template <int DH, int P, int NW, int EB, int PPS>
 struct MmaCfg {
     static constexpr int kTP = P * PPS;                          // tokens per stage
     static constexpr int kRowB = DH * EB;                        // bytes per token row
@@ -127,10 +125,7 @@ struct MmaCfg {
     static constexpr int kRing = kNS * kStage;
     static constexpr int kOffBars = kRing > kMergeB ? kRing : kMergeB;
     static constexpr int kOffTag = kOffBars + 16 * kNS;
-    static constexpr int kPageScaleB = P * SB;                   // scales of one (page, head): K's P, then V's P
-    static constexpr int kOffPages = kOffTag + 4 * kNS;          // int8: bit j of word s: page j of stage s was loaded
-    static constexpr int kOffScales = (kOffPages + (SB ? 4 * kNS : 0) + 127) / 128 * 128;
-    static constexpr int kSmem = 1024 + (SB ? kOffScales + kNS * PPS * kPageScaleB : kOffPages);  // + slack to align the ring to 1024 bytes
+    static constexpr int kSmem = 1024 + kOffTag + 4 * kNS;  // + slack to align the ring to 1024 bytes
     static constexpr int kThreads = 32 * (NW + 1);
     static_assert(DH % 64 == 0 && P % 16 == 0, "shape");
     static_assert(kRowB % kBoxInner == 0 && (kBoxInner == 128 || kBoxInner == 64), "box rows");
@@ -154,19 +149,17 @@ __device__ __forceinline__ uint32_t swz(int t, int c) {
 // row's probability residual rides in row r + 8. QM: multi-token query (a
 // chunk of new tokens per sequence): the MMA rows are (token, head) pairs of
 // q_tile chunk tokens, and row i of the chunk sees keys up to its own
-// position (causal within the chunk). MOD: modified scores and masks
-// (score_mod.cuh); row sees the keys of an interval [lo, hi), and pages before
-// the first one that some row of the CTA sees are never read.
+// position (causal within the chunk). MOD (multi-token only): modified scores
+// and masks (score_mod.cuh); a row sees the keys of an interval [lo, hi), and
+// pages before the first one that some row of the CTA sees are never read.
 template <int KT, int QT, int DH, int P, int NW, bool LO, int PPS, bool QM, bool MOD = false>
 __global__ void __launch_bounds__(32 * (NW + 1), 2)
     paged_decode_mma_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v) {
     constexpr bool kFP8 = KT == KV_DTYPE_FP8_E4M3;
-    constexpr bool kI8 = KT == KV_DTYPE_INT8;
-    constexpr bool k8 = kFP8 || kI8;  // one byte per element
-    constexpr bool kNanOut = MOD || kI8;  // a NaN among a row's visible scores or values shows in its output
-    using C = MmaCfg<DH, P, NW, k8 ? 1 : 2, PPS, kI8 ? 8 : 0>;
+    using C = MmaCfg<DH, P, NW, kFP8 ? 1 : 2, PPS>;
     constexpr bool kBF16 = KT == KV_DTYPE_BF16;  // MMA operand type: bf16, else f16
+    static_assert(!MOD || (QM && !LO && !kFP8), "modified scores: multi-token query over 16-bit K/V");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
 
     const int warp = threadIdx.x >> 5;
@@ -211,8 +204,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     // load them alongside it.
     int first = chunked ? split * chunk_pages : 0;
     int tab0 = 0;
-    if (!MOD && warp == 0 && first + lane < p.max_blocks)
-        tab0 = p.block_tables[(int64_t)b * p.max_blocks + first + lane];
+    if (!MOD && warp == 0 && first + lane < p.max_blocks) tab0 = p.block_tables[(int64_t)b * p.max_blocks + first + lane];
     int len = p.seq_lens[b];
     if (len < 0 || len > p.max_blocks * P || (QM && n_q > len)) {
         if (threadIdx.x == 0 && split == 0 && p.items == nullptr && t0 == 0) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
@@ -220,29 +212,23 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     }
     // keys of this CTA: the whole sequence, or (multi-token) up to the tile's last position
     int key_end = QM ? (len > 0 ? len - n_q + t0 + nt : 0) : len;
-    // MOD: the keys that some row of this CTA sees lie in [key_begin, key_end); those that all rows see in
-    // [key_all0, key_all1) (rows of one decode query share one interval)
-    int key_begin = 0, key_all0 = 0, key_all1 = key_end, prefix = 0, first0 = 0;
+    // MOD: the keys that some row of this CTA sees lie in [first * P, key_end); those that all rows see in
+    // [key_all0, key_all1)
+    int key_all0 = 0, key_all1 = key_end, prefix = 0;
     if constexpr (MOD) {
-        if constexpr (QM) {
-            prefix = p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0;
-            const TileKeys tk = tile_keys(p, qs0 + t0, len - n_q + t0, nt, prefix, lane);
-            if (len > 0) key_end = tk.end;
-            key_begin = tk.begin;
-            key_all0 = tk.all0;
-            key_all1 = tk.all1;
-        } else {
-            key_begin = key_all0 = first_key(p, b, len - 1);
-        }
-        first0 = min(key_begin, key_end) / P;  // a decode row's chunks are counted from its first visible page
-        first += first0;
+        prefix = p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0;
+        const TileKeys tk = tile_keys(p, qs0 + t0, len - n_q + t0, nt, prefix, lane);
+        if (len > 0) key_end = tk.end;
+        key_all0 = tk.all0;
+        key_all1 = tk.all1;
+        first = min(tk.begin, key_end) / P;
         if (warp == 0 && first + lane < p.max_blocks)
             tab0 = p.block_tables[(int64_t)b * p.max_blocks + first + lane];
     }
     const int n_pages = (key_end + P - 1) / P;
-    const int n_local = chunked ? min(chunk_pages, n_pages - first) : n_pages - first;
+    const int n_local = chunked ? min(chunk_pages, n_pages - first) : n_pages - (MOD ? first : 0);
     // Partials are needed when the row has more than one chunk.
-    const bool split_mode = p.items != nullptr ? n_pages - first0 > chunk_pages : p.num_splits > 1;
+    const bool split_mode = p.items != nullptr ? n_pages > chunk_pages : p.num_splits > 1;
     if (n_local <= 0) {
         if constexpr (QM) {
             for (int e = threadIdx.x; e < nt * p.g * DH; e += blockDim.x) {
@@ -262,7 +248,6 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     const uint32_t full_bar = sbase + C::kOffBars;
     const uint32_t empty_bar = full_bar + 8 * C::kNS;
     volatile int* stage_tag = reinterpret_cast<volatile int*>(smem + C::kOffTag);
-    volatile int* stage_pages = reinterpret_cast<volatile int*>(smem + C::kOffPages);  // int8 K/V
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kNS; ++s) {
@@ -275,7 +260,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if constexpr (!k8 && !QM) {
+        if constexpr (!kFP8 && !QM) {
             if (p.k_new != nullptr && first + n_local == n_pages) {
                 if (p.cos_sin != nullptr)
                     append_new_token_rope<KT>(p, b, kvh, len, P, DH, lane);
@@ -307,38 +292,21 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
 #pragma unroll
             for (int j = 0; j < PPS; ++j) pg[j] = __shfl_sync(0xffffffffu, tab, ((base + lane) * PPS + j) & 31);
             bool valid = false;
-            int stage_good = 0;
             if (lane < cnt) {
                 const int i = base + lane;
                 const int s = i % C::kNS;
                 const int np = min(PPS, n_local - i * PPS);  // pages in this stage
                 bool in_range = true;
-                int good = 0;  // pages of the stage inside the pool
 #pragma unroll
                 for (int j = 0; j < PPS; ++j)
-                    if (j < np) {
-                        const bool in = pg[j] >= 0 && pg[j] < p.num_pages;
-                        in_range = in_range && in;
-                        good |= in ? 1 << j : 0;
-                    }
-                if constexpr (kI8) {  // page by page: the others of the stage are still read
-                    if (!in_range) raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
-                    in_range = good != 0;
-                    stage_good = good;
-                }
+                    if (j < np) in_range = in_range && pg[j] >= 0 && pg[j] < p.num_pages;
                 if (i >= C::kNS && !mbar_wait_bounded(empty_bar + 8 * s, ((i / C::kNS) - 1) & 1, kWaitLimitNs)) {
                     raise_err(p.err, KV_DEV_ERR_TIMEOUT);
                     ok = false;
                 } else if (in_range) {
                     valid = true;
                     stage_tag[s] = i;
-                    if constexpr (kI8) {
-                        stage_pages[s] = good;
-                        mbar_arrive_expect_tx(full_bar + 8 * s,
-                                              __popc(good) * (2 * C::kBoxes * C::kPageB + C::kPageScaleB));
-                    } else {
-                        mbar_arrive_expect_tx(full_bar + 8 * s, np * 2 * C::kBoxes * C::kPageB);
-                    }
+                    mbar_arrive_expect_tx(full_bar + 8 * s, np * 2 * C::kBoxes * C::kPageB);
                 } else {
                     raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
                     stage_tag[s] = -1 - i;
@@ -353,20 +321,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
             const int bb = bx % C::kBoxes;               // box of the token row
             const int page_idx = (base + pl) * PPS + j;  // page of this CTA's range
             const int pgl = __shfl_sync(0xffffffffu, tab, page_idx & 31);
-            bool load = pl < cnt && ((vmask >> pl) & 1u) && page_idx < n_local;
-            if constexpr (kI8) {
-                load = load && pgl >= 0 && pgl < p.num_pages;
-                // the scales of page spg of stage sst: one bulk copy per lane
-                const int sst = lane / PPS, spg = lane % PPS;
-                const int g_all = __shfl_sync(0xffffffffu, stage_good, sst & 31);
-                const int page_s = __shfl_sync(0xffffffffu, tab, ((base + sst) * PPS + spg) & 31);
-                if (sst < cnt && ((vmask >> sst) & 1u) && ((g_all >> spg) & 1)) {
-                    const int s = (base + sst) % C::kNS;
-                    bulk_g2s(sbase + C::kOffScales + (s * PPS + spg) * C::kPageScaleB,
-                             p.kv_scales + ((int64_t)page_s * p.H_kv + kvh) * (2 * P), C::kPageScaleB, full_bar + 8 * s);
-                }
-            }
-            if (load) {
+            if (pl < cnt && ((vmask >> pl) & 1u) && page_idx < n_local) {
                 const int s = (base + pl) % C::kNS;
                 const uint32_t dst =
                     sbase + s * C::kStage + (is_v ? C::kChunk : 0) + bb * C::kBoxB + j * C::kPageB;
@@ -408,22 +363,17 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
         for (int h = 0; h < 2; ++h) key_lim[h] = len - n_q + t0 + (hs * 16 + r0 + 8 * h) / p.g + 1;
     }
     // MOD: first visible key, position and bias slope (log2 units per token) of rows r0 and r0 + 8
-    int key_lo[2] = {0, 0}, qpos[2] = {len - 1, len - 1};
+    int key_lo[2] = {0, 0}, qpos[2] = {0, 0};
     float slope[2] = {0.f, 0.f};
     if constexpr (MOD) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = r0 + 8 * h;
             if (r >= rows) continue;
-            const int rr = hs * 16 + r;
-            if constexpr (QM) {
-                const int tr = rr / p.g;
-                qpos[h] = len - n_q + t0 + tr;
-                key_lim[h] = max(key_lim[h], prefix);
-                key_lo[h] = first_key(p, qs0 + t0 + tr, qpos[h]);
-            } else {
-                key_lo[h] = key_begin;
-            }
+            const int rr = hs * 16 + r, tr = rr / p.g;
+            qpos[h] = len - n_q + t0 + tr;
+            key_lim[h] = max(key_lim[h], prefix);
+            key_lo[h] = first_key(p, qs0 + t0 + tr, qpos[h]);
             if (p.alibi_slopes != nullptr) slope[h] = p.alibi_slopes[kvh * p.g + rr % p.g] * kLog2e;
         }
     }
@@ -441,7 +391,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                 for (int ch = 0; ch < 2; ++ch) {
                     // 16-bit K/V: k-step kk covers dims kk*16 .. +15 in ldmatrix order. E4M3: the
                     // thread's K words hold dims quad*Dh/4 + 4*kk .. +3, so its q pairs follow them.
-                    const int d = k8 ? quad * (DH / 4) + 4 * kk + 2 * ch : kk * 16 + ch * 8 + 2 * quad;
+                    const int d = kFP8 ? quad * (DH / 4) + 4 * kk + 2 * ch : kk * 16 + ch * 8 + 2 * quad;
                     uint32_t v = (r < rows) ? q32[(q_row(r) * DH + d) >> 1] : 0u;
                     if constexpr (kFP8 && QT == KV_DTYPE_BF16)  // bf16 q -> f16 operands (exact in f16's range)
                         v = pack2_satfinite_f16(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -451,40 +401,10 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
         }
     }
 
-    // int8 K/V: the QK products run in f16 (codes are exact there). A bf16 q row is first divided by a power of
-    // two that brings its largest magnitude to 2^14 (exact but for elements 2^-38 below it, whose rounding is at
-    // most 2^-39 of the largest), and its scores are multiplied by the same power: the whole bf16 range works.
-    float q_pow[2] = {1.f, 1.f};
-    if constexpr (kI8 && QT == KV_DTYPE_BF16) {
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int kk = 0; kk < C::kKSteps; ++kk)
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    const uint32_t v = qa[kk][rr + 2 * ch];
-                    top = max(top, max((v << 16) & 0x7fffffffu, v & 0x7fff0000u));
-                }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int ex = max(static_cast<int>(top >> 23) - 127, -100);  // floor(log2(largest)); 128: inf or NaN
-            const float down = __int_as_float((14 - ex + 127) << 23);
-            q_pow[rr] = __int_as_float((ex - 14 + 127) << 23);
-#pragma unroll
-            for (int kk = 0; kk < C::kKSteps; ++kk)
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    const uint32_t v = qa[kk][rr + 2 * ch];
-                    qa[kk][rr + 2 * ch] = pack2<false>(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
-                }
-        }
-    }
-
     // Fused rotary embedding of q at position len - 1, with the same fp32 operations and rounding as
     // kv_rope_append. In the fragment a register holds dims (d, d + 1), d = kk*16 + ch*8 + 2*quad; the
     // split-halves partner d + Dh/2 sits in k-step kk + Dh/32 of the same thread.
-    if constexpr (!k8 && !QM && !MOD) {
+    if constexpr (!kFP8 && !QM) {
         const int pos = len - 1;
         if (p.cos_sin != nullptr && pos >= 0 && pos < p.max_pos) {
             const float* crow = p.cos_sin + (int64_t)pos * DH;
@@ -535,12 +455,41 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     float m_ref[2] = {-INFINITY, -INFINITY};  // reference max (log2 units) of rows r0, r0 + 8
     float l_part[2] = {0.f, 0.f};             // this lane's share of the row sums
     const float sl2 = kFP8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
-    const float sl2r[2] = {sl2 * q_pow[0], sl2 * q_pow[1]};  // int8 K/V
     bool ok = true;
+
+    // MOD: earlier accumulations are summed in the output rows (kFlushKeys, score_mod.cuh); a thread
+    // reads back what it wrote itself (q_tile * g rows take three or four 16-row slices: one warp per row)
+    constexpr int kFlush = kFlushKeys / C::kTP;
+    bool flushed = false;
+    float sum_scale[2] = {1.f, 1.f};
+    auto sum_row = [&](int h, int n) {
+        return reinterpret_cast<float2*>(p.out + q_row(r0 + 8 * h) * DH + n * 8 + 2 * quad);
+    };
 
     if (active) {
         const int n_st = (n_local + PPS - 1) / PPS;
         for (int i = wp; i < n_st; i += p.WP) {
+            if constexpr (MOD) {
+                if (i > 0 && i % kFlush == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (r0 + 8 * h < rows) {
+#pragma unroll
+                            for (int n = 0; n < C::kOT; ++n) {
+                                float2 v = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+                                if (flushed) {
+                                    const float2 w = *sum_row(h, n);
+                                    v = make_float2(fmaf(w.x, sum_scale[h], v.x), fmaf(w.y, sum_scale[h], v.y));
+                                }
+                                *sum_row(h, n) = v;
+                                o[n][2 * h] = o[n][2 * h + 1] = 0.f;
+                            }
+                        }
+                        sum_scale[h] = 1.f;
+                    }
+                    flushed = true;
+                }
+            }
             const int s = i % C::kNS;
             if (!mbar_wait_bounded(full_bar + 8 * s, (i / C::kNS) & 1, kWaitLimitNs)) {
                 raise_err(p.err, KV_DEV_ERR_TIMEOUT);
@@ -563,7 +512,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
 #pragma unroll
                 for (int n = 0; n < C::kNT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
                 const int mi = lane >> 3, rr8 = lane & 7;
-                if constexpr (k8) {
+                if constexpr (kFP8) {
                     // token r0 of each n-tile: the thread's Dh/4 bytes of that row (E4M3 -> f16 pairs)
 #pragma unroll
                     for (int n = 0; n < C::kNT; ++n) {
@@ -577,10 +526,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
 #pragma unroll
                         for (int kk = 0; kk < C::kKSteps; ++kk) {
                             uint32_t b0, b1;
-                            if constexpr (kI8)
-                                s8x4_to_f16x2x2(w[kk], b0, b1);
-                            else
-                                e4m3x4_to_f16x2x2(w[kk], b0, b1);
+                            e4m3x4_to_f16x2x2(w[kk], b0, b1);
                             mma_16816<false>(sc[n], qa[kk], b0, b1);
                         }
                     }
@@ -613,32 +559,18 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                     const int kbase = (first + i * PPS) * P;
                     tlo[0] = key_lo[0] - kbase;
                     tlo[1] = key_lo[1] - kbase;
-                    modify_scores<C::kNT, LO>(p, sc, slope, qpos[0] - kbase - 2 * quad, qpos[1] - kbase - 2 * quad);
+                    modify_rows<C::kNT>(p, sc, slope, qpos[0] - kbase - 2 * quad, qpos[1] - kbase - 2 * quad);
                 }
-                const unsigned sS = kI8 ? sbase + C::kOffScales + s * (PPS * C::kPageScaleB) : 0u;
-                const int pages_in = kI8 ? stage_pages[s] : 0;
 #pragma unroll
-                for (int n = 0; n < C::kNT; ++n) {
-                    float2 ks = make_float2(1.f, 1.f);
-                    bool in = true;
-                    if constexpr (kI8) {  // tokens n*8 + 2 quad, + 1: page n*8 / P of the stage, slot n*8 % P + 2 quad
-                        ks = lds_float2(sS + (n * 8 / P) * C::kPageScaleB + (n * 8 % P + 2 * quad) * 4);
-                        in = (pages_in >> (n * 8 / P)) & 1;
-                    }
+                for (int n = 0; n < C::kNT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int t = n * 8 + 2 * quad + (e & 1);
-                        float v;
-                        if constexpr (MOD)
-                            v = (t < tlim[e >> 1] && t >= tlo[e >> 1]) ? sc[n][e] : -INFINITY;
-                        else if constexpr (kI8)
-                            v = (in && t < tlim[e >> 1]) ? sc[n][e] * (((e & 1) ? ks.y : ks.x) * sl2r[e >> 1]) : -INFINITY;
-                        else
-                            v = (t < tlim[e >> 1]) ? sc[n][e] * sl2 : -INFINITY;
+                        const bool in = t < tlim[e >> 1] && (!MOD || t >= tlo[e >> 1]);
+                        const float v = in ? (MOD ? sc[n][e] : sc[n][e] * sl2) : -INFINITY;
                         sc[n][e] = v;
                         mx[e >> 1] = fmaxf(mx[e >> 1], v);
                     }
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
@@ -654,6 +586,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                         a[h] = (mn == m_ref[h]) ? 1.f : exp2f(m_ref[h] - mn);
                         m_ref[h] = mn;
                         l_part[h] *= a[h];
+                        if (MOD) sum_scale[h] *= a[h];
                     }
                     if constexpr (lo_rows) a[1] = a[0];  // rows r0 + 8 hold row r0's residual sums
 #pragma unroll
@@ -681,23 +614,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                         pv[e] = (sc[n][e] == -INFINITY) ? 0.f : exp2f(sc[n][e] - mr);
                         l_part[e >> 1] += pv[e];
                     }
-                    if constexpr (kI8) {
-                        // the V scales ride in the probabilities; the product runs in bf16, whose range holds any
-                        // scale (codes are exact there). A masked token's scale may be anything: its weight is 0.
-                        const float2 vs =
-                            lds_float2(sS + (n * 8 / P) * C::kPageScaleB + (P + n * 8 % P + 2 * quad) * 4);
-#pragma unroll
-                        for (int e = 0; e < (lo_rows ? 2 : 4); ++e) {
-                            const float w = pv[e] * ((e & 1) ? vs.y : vs.x);
-                            pv[e] = (sc[n][e] == -INFINITY) ? 0.f : w;
-                        }
-                        if constexpr (lo_rows) {
-                            pack2_split<true>(pv[0], pv[1], pa[n >> 1][(n & 1) * 2 + 0], pa[n >> 1][(n & 1) * 2 + 1]);
-                        } else {
-                            pack2_split<true>(pv[0], pv[1], pa[n >> 1][(n & 1) * 2 + 0], pr[n >> 1][(n & 1) * 2 + 0]);
-                            pack2_split<true>(pv[2], pv[3], pa[n >> 1][(n & 1) * 2 + 1], pr[n >> 1][(n & 1) * 2 + 1]);
-                        }
-                    } else if constexpr (lo_rows) {
+                    if constexpr (lo_rows) {
                         pack2_split<kBF16>(pv[0], pv[1], pa[n >> 1][(n & 1) * 2 + 0], pa[n >> 1][(n & 1) * 2 + 1]);
                     } else {
                         pack2_split<kBF16>(pv[0], pv[1], pa[n >> 1][(n & 1) * 2 + 0], pr[n >> 1][(n & 1) * 2 + 0]);
@@ -705,19 +622,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                     }
                 }
                 // ---- tail page: zero V rows past the length (they may hold stale data)
-                if constexpr (MOD && !QM) {  // and those before the first visible key (the same for the whole warp)
-                    const int n0 = min(key_begin - (first + i * PPS) * P, nvalid);
-                    if (n0 > 0) {
-                        constexpr int kCPR = C::kBoxInner / 16;
-                        for (int idx = lane; idx < n0 * C::kBoxes * kCPR; idx += 32) {
-                            const int t = idx / (C::kBoxes * kCPR), rem = idx % (C::kBoxes * kCPR);
-                            sts128_zero(sV + (rem / kCPR) * C::kBoxB + t * C::kBoxInner + ((rem % kCPR) << 4));
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
-                if (!kI8 && nvalid < C::kTP) {
+                if (nvalid < C::kTP) {
                     constexpr int kCPR = C::kBoxInner / 16;  // 16-byte chunks per box row
                     for (int idx = lane; idx < (C::kTP - nvalid) * C::kBoxes * kCPR; idx += 32) {
                         const int t = nvalid + idx / (C::kBoxes * kCPR);
@@ -732,7 +637,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                 // stage holds one (rare), those elements are taken as 0 in the product and added to the rows that
                 // see them.
                 bool spoiled = false;
-                if constexpr (MOD && QM) {
+                if constexpr (MOD) {
                     const int kbase = (first + i * PPS) * P;
                     if (kbase < key_all0 || kbase + C::kTP > key_all1) {
                         constexpr int kChunks = C::kChunk / 16;
@@ -758,7 +663,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                     }
                 }
                 // ---- O += P V (k = tokens, n = dims)
-                if constexpr (k8) {
+                if constexpr (kFP8) {
                     // Dim n-tile j, column r0 is dim r0 * Dh/8 + j: the thread reads its Dh/8 bytes of
                     // tokens 2q, 2q + 1, 2q + 8, 2q + 9 and pairs the two tokens' bytes per dim.
                     constexpr int kW = DH / 32;  // words per token row per thread
@@ -782,18 +687,13 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                             for (int hh = 0; hh < 2; ++hh) {  // bytes 0-1 or 2-3 of word m
                                 const uint32_t sel = hh ? 0x7362u : 0x5140u;
                                 uint32_t b0[2], b1[2];  // [dim n-tile 4m + 2hh + e]
-                                if constexpr (kI8) {
-                                    s8x4_to_bf16x2x2(byte_perm(wv[0][m], wv[1][m], sel), b0[0], b0[1]);
-                                    s8x4_to_bf16x2x2(byte_perm(wv[2][m], wv[3][m], sel), b1[0], b1[1]);
-                                } else {
                                 e4m3x4_to_f16x2x2(byte_perm(wv[0][m], wv[1][m], sel), b0[0], b0[1]);  // tokens 2q, 2q + 1
                                 e4m3x4_to_f16x2x2(byte_perm(wv[2][m], wv[3][m], sel), b1[0], b1[1]);  // tokens 2q + 8, + 9
-                                }
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
                                     const int j = 4 * m + 2 * hh + e;
-                                    mma_16816<kI8>(o[j], pa[ks], b0[e], b1[e]);
-                                    if constexpr (!lo_rows) mma_16816<kI8>(o[j], pr[ks], b0[e], b1[e]);
+                                    mma_16816<false>(o[j], pa[ks], b0[e], b1[e]);
+                                    if constexpr (!lo_rows) mma_16816<false>(o[j], pr[ks], b0[e], b1[e]);
                                 }
                             }
                         }
@@ -807,7 +707,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                         const int c = op * 2 + (mi >> 1);
                         uint32_t v0, v1, v2, v3;
                         ldsm_x4_trans(sV + (c >> 3) * C::kBoxB + t * 128 + (((c & 7) ^ (t & 7)) << 4), v0, v1, v2, v3);
-                        if constexpr (MOD && QM) {
+                        if constexpr (MOD) {
                             if (spoiled) {
                                 v0 ^= nonfinite16<kBF16>(v0), v1 ^= nonfinite16<kBF16>(v1);
                                 v2 ^= nonfinite16<kBF16>(v2), v3 ^= nonfinite16<kBF16>(v3);
@@ -843,13 +743,23 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
             if (r < rows) {
                 float* dst = merge + (cw * 16 + r) * (DH + 2);
                 const float vs = kFP8 ? p.v_scale[kvh] : 1.f;
+                if constexpr (MOD) {
+                    if (flushed) {
+#pragma unroll
+                        for (int n = 0; n < C::kOT; ++n) {
+                            const float2 w = *sum_row(h, n);
+                            o[n][2 * h] = fmaf(w.x, sum_scale[h], o[n][2 * h]);
+                            o[n][2 * h + 1] = fmaf(w.y, sum_scale[h], o[n][2 * h + 1]);
+                        }
+                    }
+                }
                 // a NaN sum keeps its place in the merge whatever the row's maximum is
-                if (kNanOut && l_part[h] != l_part[h]) m_ref[h] = m_ref[h] == -INFINITY ? 0.f : m_ref[h];
+                if (MOD && l_part[h] != l_part[h] && m_ref[h] == -INFINITY) m_ref[h] = 0.f;
 #pragma unroll
                 for (int n = 0; n < C::kOT; ++n) {
                     // column 2q (+1) of dim n-tile n: dim n*8 + 2q (+1); E4M3: dim (2q (+1)) * Dh/8 + n
-                    const int d0 = k8 ? (2 * quad) * (DH / 8) + n : n * 8 + 2 * quad;
-                    const int d1 = k8 ? (2 * quad + 1) * (DH / 8) + n : n * 8 + 2 * quad + 1;
+                    const int d0 = kFP8 ? (2 * quad) * (DH / 8) + n : n * 8 + 2 * quad;
+                    const int d1 = kFP8 ? (2 * quad + 1) * (DH / 8) + n : n * 8 + 2 * quad + 1;
                     dst[d0] = (o[n][2 * h] + (lo_rows ? o[n][2] : 0.f)) * vs;
                     dst[d1] = (o[n][2 * h + 1] + (lo_rows ? o[n][3] : 0.f)) * vs;
                 }
@@ -886,17 +796,12 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
             // An infinity among the values the row sees meets a probability's residual, which may be 0 or negative:
             // a NaN. Where a sum is NaN and the weights are not (rare), the row's values say what it is.
             if (U != U && L == L) {
-                int lo = key_begin, hi = min(key_end, (first + n_local) * P);
-                if constexpr (QM) {
-                    const int pos = len - n_q + t0 + hh / p.g;
-                    lo = first_key(p, qs0 + t0 + hh / p.g, pos);
-                    hi = max(pos + 1, prefix);
-                }
-                U = sum_nonfinite<kBF16>(p, b, kvh, P, DH, d, max(lo, first * P), hi);
+                const int tr = hh / p.g, pos = len - n_q + t0 + tr;
+                U = sum_nonfinite<kBF16>(p, b, kvh, P, DH, d, first_key(p, qs0 + t0 + tr, pos), max(pos + 1, prefix));
             }
         }
         if (!split_mode) {
-            p.out[hq * DH + d] = (kNanOut ? L != 0.f : L > 0.f) ? U / L : 0.f;
+            p.out[hq * DH + d] = (MOD ? L != 0.f : L > 0.f) ? U / L : 0.f;
         } else {
             const int64_t ps = p.items != nullptr ? (int64_t)item * p.g + hh : hq * p.num_splits + split;
             p.part_u[ps * DH + d] = U;

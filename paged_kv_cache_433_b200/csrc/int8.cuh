@@ -30,9 +30,9 @@ __device__ __forceinline__ void s8x4_to_bf16x2x2(uint32_t w, uint32_t& lo, uint3
     asm("sub.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b & 0xff7fff7fu), "r"(b & 0xff80ff80u));
 }
 
-__device__ __forceinline__ float2 lds_float2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ float lds_float(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 

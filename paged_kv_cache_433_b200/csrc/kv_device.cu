@@ -624,7 +624,7 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
             S = (nb + C - 1) / C;
         }
     }
-    const bool new_op = ex.mod || dtype == KV_DTYPE_INT8;  // on the warp-MMA kernel only
+    const bool new_op = ex.mod || dtype == KV_DTYPE_INT8;  // on the heads-as-columns kernel (decode_cols.cuh) only
     const bool tc = mma && !new_op && tc_ok(dtype, g, Dh, cos_sin != nullptr, B, H_kv, num_splits);
     const bool planned = tc ? planned_tc(B, num_splits) : planned_ok(mma, B, H_q, H_kv, num_splits);
 
@@ -738,8 +738,8 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) ||
             !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
             return KV_ERR_CUDA;
-        e = ex.mod                   ? launch_mma_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
-            : dtype == KV_DTYPE_INT8 ? launch_mma_int8(p, tk, tv, q_dtype, Dh, page_size, grid, st)
+        e = ex.mod                   ? launch_cols_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
+            : dtype == KV_DTYPE_INT8 ? launch_cols_int8(p, tk, tv, q_dtype, Dh, page_size, grid, st)
             : dtype == KV_DTYPE_BF16 ? launch_mma_bf16(p, tk, tv, Dh, page_size, grid, st)
             : dtype == KV_DTYPE_F16 ? launch_mma_f16(p, tk, tv, Dh, page_size, grid, st)
                                     : launch_mma_fp8(p, tk, tv, q_dtype, Dh, page_size, grid, st);

@@ -41,10 +41,38 @@ struct NormRopeParams {
     int32_t max_pos, style, q_rows, H_kv, Dh, P;
 };
 
+// A 16-byte vector as pairs of fp32 values, and back (rounded to nearest even).
+template <int DT, int H>
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&x)[H]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == KV_DTYPE_F32) {
+        x[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        x[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == KV_DTYPE_BF16)
+                x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else
+                x[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        }
+    }
+}
+template <int DT, int H>
+__device__ __forceinline__ uint4 pack(const float2 (&x)[H]) {
+    if constexpr (DT == KV_DTYPE_F32)
+        return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+    else
+        return make_uint4(pack2<DT == KV_DTYPE_BF16>(x[0].x, x[0].y), pack2<DT == KV_DTYPE_BF16>(x[1].x, x[1].y),
+                          pack2<DT == KV_DTYPE_BF16>(x[2].x, x[2].y), pack2<DT == KV_DTYPE_BF16>(x[3].x, x[3].y));
+}
+
+constexpr int kNormRopeThreads = 384, kNormRopeCtas = 2;  // per CTA, per SM
+
 template <int DT>
-__global__ void __launch_bounds__(384) kv_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
-    using V = RopeVec<DT>;
-    constexpr int N = V::kN;  // elements per 16-byte vector
+__global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas) kv_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int N = RopeVec<DT>::kN;  // elements per 16-byte vector
+    constexpr int H = N / 2;
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
     const int32_t Dh = p.Dh;
@@ -64,11 +92,12 @@ __global__ void __launch_bounds__(384) kv_norm_rope_append_kernel(const __grid_c
         const uint4* src = (is_q ? p.q : (is_v ? p.v_new : p.k_new)) + (int64_t)h * vpr;
         const int64_t stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
         const float* w = is_q ? p.q_weight : p.k_weight;
-        float wa[N], wb[N];
+        float2 wa[H], wb[H];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            wa[i] = !is_v && w != nullptr ? w[va * N + i] : 1.f;
-            wb[i] = !is_v && w != nullptr ? w[vb * N + i] : 1.f;
+        for (int i = 0; i < H; ++i) {
+            const bool weighted = !is_v && w != nullptr;
+            wa[i] = weighted ? make_float2(w[va * N + 2 * i], w[va * N + 2 * i + 1]) : make_float2(1.f, 1.f);
+            wb[i] = weighted ? make_float2(w[vb * N + 2 * i], w[vb * N + 2 * i + 1]) : make_float2(1.f, 1.f);
         }
         int64_t b = blockIdx.x;
         if (b >= p.B) continue;
@@ -104,39 +133,55 @@ __global__ void __launch_bounds__(384) kv_norm_rope_append_kernel(const __grid_c
                     p.v_pages[cache_row + vb] = c;
                 }
             } else if (pos_ok) {
-                float xa[N], xb[N];
-                V::load(a, xa);
-                V::load(c, xb);
-                float ss = 0.f;
+                // pairs of neighbouring elements go through the packed fp32 operations
+                float2 xa[H], xb[H], cs[H], sn[H];
+                unpack<DT>(a, xa);
+                unpack<DT>(c, xb);
+                float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < N; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+                for (int i = 0; i < H; ++i) sq = ffma2(xa[i], xa[i], ffma2(xb[i], xb[i], sq));
+                float ss = sq.x + sq.y;
+                const float* crow = p.cos_sin + (int64_t)pos * Dh;
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    const float4 cc = __ldg(reinterpret_cast<const float4*>(crow + k0 + 2 * i));
+                    const float4 si = __ldg(reinterpret_cast<const float4*>(crow + Dh / 2 + k0 + 2 * i));
+                    cs[i] = make_float2(cc.x, cc.y), cs[i + 1] = make_float2(cc.z, cc.w);
+                    sn[i] = make_float2(si.x, si.y), sn[i + 1] = make_float2(si.z, si.w);
+                }
                 for (int o = upr >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(row_mask, ss, o);
                 const float rs = rsqrtf(ss * p.inv_dh + p.eps);
+                // 1 / rms joins the angles' cosines and sines: one product fewer per element
+                const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    xa[i] *= rs * wa[i];
-                    xb[i] *= rs * wb[i];
-                }
-                const float* crow = p.cos_sin + (int64_t)pos * Dh;
-                float cs[N], sn[N];
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float4 cc = __ldg(reinterpret_cast<const float4*>(crow + k0 + i));
-                    const float4 si = __ldg(reinterpret_cast<const float4*>(crow + Dh / 2 + k0 + i));
-                    cs[i] = cc.x, cs[i + 1] = cc.y, cs[i + 2] = cc.z, cs[i + 3] = cc.w;
-                    sn[i] = si.x, sn[i + 1] = si.y, sn[i + 2] = si.z, sn[i + 3] = si.w;
+                for (int i = 0; i < H; ++i) {
+                    xa[i] = fmul2(xa[i], wa[i]);
+                    xb[i] = fmul2(xb[i], wb[i]);
+                    cs[i] = fmul2(cs[i], rs2);
+                    sn[i] = fmul2(sn[i], rs2);
                 }
                 if (p.style == KV_ROPE_HALF) {
+                    // pair k0 + e = (element e of a, element e of b)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) rotate_pair(xa[i], xb[i], cs[i], sn[i]);
+                    for (int i = 0; i < H; ++i) {
+                        const float2 ns = make_float2(-sn[i].x, -sn[i].y);
+                        const float2 t = ffma2(xa[i], cs[i], fmul2(xb[i], ns));
+                        xb[i] = ffma2(xb[i], cs[i], fmul2(xa[i], sn[i]));
+                        xa[i] = t;
+                    }
                 } else {
+                    // a holds pairs k0 .. k0 + H - 1 as neighbours, b the next H
+                    auto turn = [](float2 x, float c1, float s1) {
+                        return ffma2(x, make_float2(c1, c1), fmul2(make_float2(x.y, x.x), make_float2(-s1, s1)));
+                    };
 #pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        rotate_pair(xa[2 * i], xa[2 * i + 1], cs[i], sn[i]);
-                        rotate_pair(xb[2 * i], xb[2 * i + 1], cs[N / 2 + i], sn[N / 2 + i]);
+                    for (int i = 0; i < H; ++i) {
+                        xa[i] = turn(xa[i], i & 1 ? cs[i / 2].y : cs[i / 2].x, i & 1 ? sn[i / 2].y : sn[i / 2].x);
+                        const int k = i + H;
+                        xb[i] = turn(xb[i], k & 1 ? cs[k / 2].y : cs[k / 2].x, k & 1 ? sn[k / 2].y : sn[k / 2].x);
                     }
                 }
-                const uint4 ya = V::store(xa), yb = V::store(xb);
+                const uint4 ya = pack<DT>(xa), yb = pack<DT>(xb);
                 if (is_q) {
                     uint4* dst = p.q_out + (b * p.q_rows + h) * vpr;
                     dst[va] = ya;
@@ -229,12 +274,12 @@ extern "C" int kv_norm_rope_append(void* k_pages, void* v_pages, void* q_out, vo
     p.P = page_size;
     const int64_t units = (static_cast<int64_t>(p.q_rows) + H_kv + (cache ? H_kv : 0)) * (vpr / 2);
     if (units > 0x7fffffffLL) return KV_ERR_UNSUPPORTED;
-    const int threads = static_cast<int>(std::min<int64_t>(384, (units + 31) / 32 * 32));
+    const int threads = static_cast<int>(std::min<int64_t>(kNormRopeThreads, (units + 31) / 32 * 32));
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         return KV_ERR_CUDA;
-    const int64_t blocks = std::min<int64_t>(B, static_cast<int64_t>(sms) * std::max(1, 1152 / threads));  // resident CTAs
+    const int64_t blocks = std::min<int64_t>(B, static_cast<int64_t>(sms) * std::max(1, kNormRopeThreads * kNormRopeCtas / threads));  // resident CTAs
     auto run = [&](auto kernel) {
         return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, static_cast<cudaStream_t>(stream),
                           p);

@@ -103,6 +103,21 @@ struct PfCfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
+// row[0..31] = row * scale (if `more`) + a: accumulator columns onto the sums that an output row holds.
+__device__ __forceinline__ void add_to_row(float* row, const uint32_t (&a)[32], float scale, bool more) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float4* at = reinterpret_cast<float4*>(row + i);
+        float4 v = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]), __uint_as_float(a[i + 2]),
+                               __uint_as_float(a[i + 3]));
+        if (more) {
+            const float4 o = *at;
+            v = make_float4(fmaf(o.x, scale, v.x), fmaf(o.y, scale, v.y), fmaf(o.z, scale, v.z), fmaf(o.w, scale, v.w));
+        }
+        *at = v;
+    }
+}
+
 template <int KT, int DH, int P, bool MOD = false>
 __global__ void __launch_bounds__(384, 1)
     paged_prefill_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
@@ -111,6 +126,7 @@ __global__ void __launch_bounds__(384, 1)
     constexpr bool kBF16 = KT == KV_DTYPE_BF16;
     constexpr uint32_t kIdescQK = idesc_f16(kBF16, 128, C::kTP, false, false);
     constexpr uint32_t kIdescPV = idesc_f16(kBF16, 128, DH, false, true);
+    constexpr int kFlush = kFlushKeys / C::kTP;  // MOD: stages whose P.V share one accumulation
     extern __shared__ __align__(1024) unsigned char smem_raw[];
 
     const int warp = threadIdx.x >> 5;
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
                         umma_ts(tO, tP + kk * 8, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128), kIdescPV,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                                ((MOD ? j % kFlush != 0 : j > 0) || kk > 0) ? 1u : 0u);
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
                         umma_ts(tO, tP + C::kTP / 2 + kk * 8, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128),
@@ -396,6 +412,7 @@ __global__ void __launch_bounds__(384, 1)
         };
         const float sl2 = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
+        float sum_scale = 1.f;  // MOD: the factor from the sums kept in the output row to the current reference
         constexpr int kH = C::kTP / 2;       // key columns per thread
         // lanes 0 .. kPPS-1: the page ids of stage j, read one stage ahead; the mask of pages the producers
         // skip (entries outside the pool) is then known without waiting for the V entry
@@ -452,7 +469,8 @@ __global__ void __launch_bounds__(384, 1)
                 m_ref = mx2;
                 l *= alpha;
             }
-            if (j > 0 && __any_sync(0xffffffffu, need)) {
+            const bool flush = MOD && j > 0 && j % kFlush == 0;
+            if (flush || (j > 0 && __any_sync(0xffffffffu, need))) {
                 // O holds P.V of the earlier stages: wait for the last one, then rescale this half of the rows
                 if (!wait(okl, p_empty((j - 1) % 3), ((j - 1) / 3) & 1)) {
                     ok = false;  // the next meeting stops the pair
@@ -465,12 +483,19 @@ __global__ void __launch_bounds__(384, 1)
                     uint32_t a[32];
                     tmem_ld32(tO + lane_addr + half * kH + q2 * 32, a);
                     tmem_wait_ld();
+                    if (flush) {  // P.V of this stage starts a new accumulation
+                        if (row_valid)
+                            add_to_row(p.out + qrow * DH + half * kH + q2 * 32, a, sum_scale, j > kFlush);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * alpha);
-                    tmem_st32(tO + lane_addr + half * kH + q2 * 32, a);
+                        for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * alpha);
+                        tmem_st32(tO + lane_addr + half * kH + q2 * 32, a);
+                    }
                 }
                 tmem_wait_st();
+                if (flush) sum_scale = 1.f;
             }
+            if (MOD) sum_scale *= alpha;
             // probabilities -> P over this S buffer: hi pairs in columns 0..63, residual pairs in 64..127
             // (this thread's keys: hi columns 32 half .., lo columns 64 + 32 half ..)
             const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref;
@@ -557,6 +582,18 @@ __global__ void __launch_bounds__(384, 1)
             tmem_ld32(tO + lane_addr + half * kH + 32, b2);
             tmem_wait_ld();
             if constexpr (MOD) {
+                if (n_st > kFlush && row_valid) {  // the sums of the earlier accumulations
+                    const float4* sums = reinterpret_cast<const float4*>(dst);
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 v = sums[i / 4];
+                        uint32_t* x = i < 32 ? a + i : b2 + i - 32;
+                        x[0] = __float_as_uint(fmaf(v.x, sum_scale, __uint_as_float(x[0])));
+                        x[1] = __float_as_uint(fmaf(v.y, sum_scale, __uint_as_float(x[1])));
+                        x[2] = __float_as_uint(fmaf(v.z, sum_scale, __uint_as_float(x[2])));
+                        x[3] = __float_as_uint(fmaf(v.w, sum_scale, __uint_as_float(x[3])));
+                    }
+                }
                 // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for
                 // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
                 // values, read again, say what those sums are.

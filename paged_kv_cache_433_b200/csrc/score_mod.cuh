@@ -73,47 +73,59 @@ __device__ __forceinline__ float2 cap_small2(const DecodeParams& p, float2 x) {
     return fmul2(x, r);
 }
 
-// Products q . k of one warp's MMA tiles -> modified scores. sc[n][e]: row h = e / 2, token n * 8 + (e & 1) of the
-// stage counted from the lane's first; dist0 / dist1: position minus that first token for rows 0 / 1. LO: only
-// row 0 is real.
-template <int NT, bool LO>
-__device__ __forceinline__ void modify_scores(const DecodeParams& p, float (&sc)[NT][4], const float (&slope)[2],
-                                              int dist0, int dist1) {
-    constexpr int E = LO ? 2 : 4;
+// x[0 .. 1] of every pair: products -> capped (or only scaled) scores in log2 units. Called by whole warps.
+template <int N>
+__device__ __forceinline__ void cap_scores(const DecodeParams& p, float (&x)[N]) {
     if (p.cap_out != 0.f) {
         float big = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(sc[n][e]));
+        for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(x[c]));
         if (__any_sync(0xffffffffu, big > p.cap_small)) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < E; ++e) sc[n][e] = tanh_any(sc[n][e] * p.cap_in) * p.cap_out;
+            for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c] * p.cap_in) * p.cap_out;
         } else {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 t = cap_small2(p, make_float2(sc[n][e], sc[n][e + 1]));
-                    sc[n][e] = t.x;
-                    sc[n][e + 1] = t.y;
-                }
+            for (int c = 0; c < N; c += 2) {
+                const float2 t = cap_small2(p, make_float2(x[c], x[c + 1]));
+                x[c] = t.x;
+                x[c + 1] = t.y;
+            }
         }
     } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < E; ++e) sc[n][e] *= p.scale_log2;
+        for (int c = 0; c < N; ++c) x[c] *= p.scale_log2;
     }
+}
+
+// Products of one warp's MMA tiles, query rows as MMA rows: sc[n][e] is row e / 2, token n * 8 + (e & 1) of the stage
+// counted from the lane's first; dist0 / dist1: position minus that first token for rows 0 / 1.
+template <int NT>
+__device__ __forceinline__ void modify_rows(const DecodeParams& p, float (&sc)[NT][4], const float (&slope)[2], int dist0,
+                                            int dist1) {
+    cap_scores(p, reinterpret_cast<float(&)[NT * 4]>(sc));
     if (p.alibi_slopes != nullptr) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = static_cast<float>((e >= 2 ? dist1 : dist0) - (n * 8 + (e & 1)));
-                sc[n][e] -= slope[e >> 1] * fabsf(d);
+            for (int e = 0; e < 4; ++e)
+                sc[n][e] -= slope[e >> 1] * fabsf(static_cast<float>((e >= 2 ? dist1 : dist0) - (n * 8 + (e & 1))));
+    }
+}
+
+// The same with heads as MMA columns: sc[nt][mt][e] is head column e & 1 of tile nt, token mt * 16 + 8 (e / 2) counted
+// from the lane's first; dist: the query's position minus that first token.
+template <int NT, int MT>
+__device__ __forceinline__ void modify_cols(const DecodeParams& p, float (&sc)[NT][MT][4], const float (&slope)[NT][2],
+                                            int dist) {
+    cap_scores(p, reinterpret_cast<float(&)[NT * MT * 4]>(sc));
+    if (p.alibi_slopes != nullptr) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float d = fabsf(static_cast<float>(dist - (mt * 16 + 8 * (e >> 1))));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sc[nt][mt][e] -= slope[nt][e & 1] * d;
             }
     }
 }
@@ -121,31 +133,19 @@ __device__ __forceinline__ void modify_scores(const DecodeParams& p, float (&sc)
 // The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key.
 template <int N>
 __device__ __forceinline__ void modify_row(const DecodeParams& p, float (&s)[N], float slope, int dist0) {
-    if (p.cap_out != 0.f) {
-        float big = 0.f;
-#pragma unroll
-        for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(s[c]));
-        if (__any_sync(0xffffffffu, big > p.cap_small)) {
-#pragma unroll
-            for (int c = 0; c < N; ++c) s[c] = tanh_any(s[c] * p.cap_in) * p.cap_out;
-        } else {
-#pragma unroll
-            for (int c = 0; c < N; c += 2) {
-                const float2 t = cap_small2(p, make_float2(s[c], s[c + 1]));
-                s[c] = t.x;
-                s[c + 1] = t.y;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < N; ++c) s[c] *= p.scale_log2;
-    }
+    cap_scores(p, s);
     if (p.alibi_slopes != nullptr) {
         const float d = static_cast<float>(dist0);
 #pragma unroll
         for (int c = 0; c < N; ++c) s[c] -= slope * fabsf(d - static_cast<float>(c));
     }
 }
+
+// The tensor core rounds each sum of 16 products and the accumulator towards zero: over n keys an accumulator loses
+// about n 2^-29 of itself (8.4e-6 at 4224 keys, 6.5e-5 at 32K, measured with warp MMA and tcgen05 alike). The
+// multi-token kernels therefore move their output accumulators into fp32 sums, kept in the output rows that the same
+// threads write at the end, after every kFlushKeys keys.
+constexpr int kFlushKeys = 2048;
 
 // ---- 16-bit values with an all-ones exponent (NaN, +-inf) -----------------
 // The halves of w that are not finite, with 0 in the place of finite ones.

@@ -287,14 +287,18 @@ class KvPrefixIndex:
 
 
 # ---------------------------------------------------------------- device calls
-def _torch_dtype_code(t) -> int:
-    import torch
+_DTYPES = {}  # torch dtype -> KV_DTYPE_* code
 
-    m = {torch.float32: KV_DTYPE_F32, torch.bfloat16: KV_DTYPE_BF16, torch.float16: KV_DTYPE_F16,
-         torch.uint8: KV_DTYPE_FP8_E4M3}
-    if t.dtype not in m:
+
+def _torch_dtype_code(t) -> int:
+    if not _DTYPES:
+        import torch
+
+        _DTYPES.update({torch.float32: KV_DTYPE_F32, torch.bfloat16: KV_DTYPE_BF16, torch.float16: KV_DTYPE_F16,
+                        torch.uint8: KV_DTYPE_FP8_E4M3})
+    if t.dtype not in _DTYPES:
         raise KvError("dtype", KV_ERR_ARG)
-    return m[t.dtype]
+    return _DTYPES[t.dtype]
 
 
 def _stream(stream) -> Optional[int]:
@@ -445,61 +449,80 @@ def paged_prefill_attention(out, q, q_start, max_q_len: int, k_pages, v_pages, b
 
 
 # ---- per-head norm + rotation + append, int8 cache, modified scores and masks
+# A decode step makes these calls once per layer and the GPU's part of a small one is a few microseconds, so the checks
+# of a tensor are one function call, and only a failed check looks for its reason.
+_torch = None  # the torch module, once a device call has imported it
+
+
+def _begin(t, name: str) -> int:
+    """Imports torch on first use; the index of the current device, on which `t` and every tensor of a call has to be."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    dev = t.get_device()
+    if dev < 0 or dev != _torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    return dev
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _here(t, name: str, shape=None, dtype=None):
-    """Pointer of a contiguous tensor on the current device, of this shape and dtype (None passes through)."""
-    if t is None:
-        return None
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    import torch
-
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if shape is not None and t.shape != shape:
+def _refuse(t, name: str, shape, dtype):
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != _torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    raise ValueError(f"{name} must be contiguous (within a token's heads, where tokens may be strided)")
+
+
+def _at(t, dev: int, name: str, shape, dtype) -> int:
+    """Pointer of a contiguous tensor of this shape and dtype on device `dev`."""
+    if t is None or t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, shape, dtype)
     return t.data_ptr()
 
 
-def _token_rows(t, name: str, shape, dtype):
+def _at_or_none(t, dev: int, name: str, shape, dtype):
+    return None if t is None else _at(t, dev, name, shape, dtype)
+
+
+def _tokens_at(t, dev: int, name: str, shape, dtype):
     """(pointer, elements from token to token) of a [B, H, Dh] tensor whose heads are contiguous within a token."""
-    import torch
-
+    if t is None or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype)
+    st, sh, sd = t.stride()
     B, H, Dh = shape
-    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(), f"{name} must be on the current CUDA device")
-    _need(t.dtype == dtype, f"{name} must be {dtype}")
-    _need(tuple(t.shape) == tuple(shape), f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need((Dh == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == Dh), f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if B > 1 else H * Dh)
+    if (sd != 1 and Dh != 1) or (sh != Dh and H != 1):
+        _refuse(t, name, shape, dtype)
+    return t.data_ptr(), (st if B > 1 else H * Dh)
 
 
-def _flag(err_flag):
-    import torch
-
+def _flag_at(err_flag, dev: int):
     if err_flag is None:
         return None
     _need(err_flag.numel() >= 1, "err_flag is empty")
-    return _here(err_flag, "err_flag", dtype=torch.int32)
+    return _at(err_flag, dev, "err_flag", err_flag.shape, _torch.int32)
 
 
-def _scratch(workspace):
-    return (None, 0) if workspace is None else (_here(workspace, "workspace"), workspace.numel() * workspace.element_size())
+def _scratch_at(workspace, dev: int):
+    if workspace is None:
+        return None, 0
+    return _at(workspace, dev, "workspace", workspace.shape, workspace.dtype), workspace.numel() * workspace.element_size()
 
 
-def _pools(k_pages, v_pages, dtypes):
-    """Shape (num_pages, H_kv, P, Dh) and pointers of a pool pair whose dtype is one of `dtypes`."""
-    _need(k_pages.dim() == 4 and k_pages.dtype in dtypes, f"the pools must be [num_pages, H_kv, P, Dh] of {dtypes}")
-    return k_pages.shape, _here(k_pages, "k_pages"), _here(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
-
-
-def _ids(t, name: str, n: int, dtype):
-    return _here(t, name, (n,), dtype) if n else None
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream().cuda_stream without the object
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def kv_norm_rope_append(k_pages, v_pages, k_new, v_new, slot_mapping, positions, cos_sin, k_weight, eps: float,
@@ -510,56 +533,55 @@ def kv_norm_rope_append(k_pages, v_pages, k_new, v_new, slot_mapping, positions,
     q [B, H_q, Dh], k/v_new [B, H_kv, Dh]: the heads of a token contiguous, tokens any stride apart (slices of one
     projection's output); q_out, k_out contiguous. k/v_pages, v_new and slot_mapping may be None together when k_out
     is given (a quantising append writes the cache then). Other arguments as kv_rope_append."""
-    import torch
-
-    B, H_kv, Dh = k_new.shape
-    dt = k_new.dtype
+    dev = _begin(k_new, "k_new")
+    dt, f32 = k_new.dtype, _torch.float32
+    kshape = B, H_kv, Dh = k_new.shape
     num_pages, kp, vp, vptr, vs, slots = 0, None, None, None, 0, None
     if k_pages is not None:
-        (num_pages, Hp, P, Dp), kp, vp = _pools(k_pages, v_pages, (dt,))
-        _need((Hp, P, Dp) == (H_kv, page_size, Dh), "the pools must be [num_pages, H_kv, page_size, Dh]")
-        vptr, vs = _token_rows(v_new, "v_new", (B, H_kv, Dh), dt)
-        slots = _ids(slot_mapping, "slot_mapping", B, torch.int64)
+        num_pages = k_pages.shape[0]
+        pshape = (num_pages, H_kv, page_size, Dh)
+        kp, vp = _at(k_pages, dev, "k_pages", pshape, dt), _at(v_pages, dev, "v_pages", pshape, dt)
+        vptr, vs = _tokens_at(v_new, dev, "v_new", kshape, dt)
+        slots = _at(slot_mapping, dev, "slot_mapping", (B,), _torch.int64)
     else:
         _need(v_pages is None and v_new is None and slot_mapping is None, "v_pages, v_new and slot_mapping need k_pages")
-    kptr, ks = _token_rows(k_new, "k_new", (B, H_kv, Dh), dt)
-    H_q, qptr, qs = 0, None, 0
+    kptr, ks = _tokens_at(k_new, dev, "k_new", kshape, dt)
+    _need((q is None) == (q_out is None), "q and q_out go together")
+    H_q, qptr, qs, qo = 0, None, 0, None
     if q is not None:
         H_q = q.shape[1]
-        qptr, qs = _token_rows(q, "q", (B, H_q, Dh), dt)
-    _need((q is None) == (q_out is None), "q and q_out go together")
-    _need(cos_sin.dim() == 2 and cos_sin.shape[1] == Dh, "cos_sin must be [max_pos, Dh]")
+        qptr, qs = _tokens_at(q, dev, "q", (B, H_q, Dh), dt)
+        qo = _at(q_out, dev, "q_out", (B, H_q, Dh), dt)
+    max_pos = cos_sin.shape[0]
     rc = lib().kv_norm_rope_append(
-        kp, vp, _here(q_out, "q_out", (B, H_q, Dh), dt), _here(k_out, "k_out", (B, H_kv, Dh), dt), qptr, kptr, vptr, qs, ks,
-        vs, _here(q_weight, "q_weight", (Dh,), torch.float32), _here(k_weight, "k_weight", (Dh,), torch.float32), float(eps),
-        slots, _ids(positions, "positions", B, torch.int32), _here(cos_sin, "cos_sin", dtype=torch.float32),
-        cos_sin.shape[0], ROPE_STYLE[style], B, H_q, H_kv, Dh, page_size, num_pages, _torch_dtype_code(k_new),
-        _flag(err_flag), _stream(stream))
+        kp, vp, qo, _at_or_none(k_out, dev, "k_out", kshape, dt), qptr, kptr, vptr, qs, ks, vs,
+        _at_or_none(q_weight, dev, "q_weight", (Dh,), f32), _at_or_none(k_weight, dev, "k_weight", (Dh,), f32), float(eps), slots,
+        _at(positions, dev, "positions", (B,), _torch.int32), _at(cos_sin, dev, "cos_sin", (max_pos, Dh), f32), max_pos,
+        ROPE_STYLE[style], B, H_q, H_kv, Dh, page_size, num_pages, _torch_dtype_code(k_new), _flag_at(err_flag, dev),
+        _raw_stream(stream, dev))
     _check("kv_norm_rope_append", rc)
 
 
-def _int8_pools(k_pages, v_pages, kv_scales):
-    import torch
-
-    shape, kp, vp = _pools(k_pages, v_pages, (torch.int8,))
-    num_pages, H_kv, P, _ = shape
-    return shape, kp, vp, _here(kv_scales, "kv_scales", (num_pages, H_kv, 2, P), torch.float32)
+def _int8_pools_at(k_pages, v_pages, kv_scales, dev: int):
+    """Shape and pointers of int8 pools [num_pages, H_kv, P, Dh] and their scales [num_pages, H_kv, 2, P]."""
+    shape = num_pages, H_kv, P, _ = k_pages.shape
+    return (shape, _at(k_pages, dev, "k_pages", shape, _torch.int8), _at(v_pages, dev, "v_pages", shape, _torch.int8),
+            _at(kv_scales, dev, "kv_scales", (num_pages, H_kv, 2, P), _torch.float32))
 
 
 def kv_append_int8(k_pages, v_pages, kv_scales, k_new, v_new, slot_mapping, page_size: int, err_flag=None,
                    stream=None) -> None:
     """Quantise k/v_new [B, H_kv, Dh] (bf16/fp16/fp32; tokens any stride apart) row by row and append them into int8
     pools [num_pages, H_kv, P, Dh] with their scales, fp32 [num_pages, H_kv, 2, P]."""
-    import torch
-
-    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    dev = _begin(k_pages, "k_pages")
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
     _need(P == page_size, "the pools' page size differs")
-    B = k_new.shape[0]
-    kptr, ks = _token_rows(k_new, "k_new", (B, H_kv, Dh), k_new.dtype)
-    vptr, vs = _token_rows(v_new, "v_new", (B, H_kv, Dh), k_new.dtype)
+    dt, B = k_new.dtype, k_new.shape[0]
+    kptr, ks = _tokens_at(k_new, dev, "k_new", (B, H_kv, Dh), dt)
+    vptr, vs = _tokens_at(v_new, dev, "v_new", (B, H_kv, Dh), dt)
     rc = lib().kv_append_int8(kp, vp, sc, kptr, vptr, ks, vs, _torch_dtype_code(k_new),
-                              _ids(slot_mapping, "slot_mapping", B, torch.int64), B, H_kv, Dh, P, num_pages,
-                              _flag(err_flag), _stream(stream))
+                              _at(slot_mapping, dev, "slot_mapping", (B,), _torch.int64), B, H_kv, Dh, P, num_pages,
+                              _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("kv_append_int8", rc)
 
 
@@ -567,28 +589,26 @@ def kv_dequant_pages_int8(k_out, v_out, k_pages, v_pages, kv_scales, src_pages, 
                           stream=None) -> None:
     """Pages src_pages[i] of the int8 pools -> pages dst_pages[i] of k/v_out [num_out_pages, H_kv, P, Dh]
     (bf16/fp16/fp32); src/dst_pages int32 (device)."""
-    import torch
-
-    shape, kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
-    num_pages, H_kv, P, Dh = shape
-    oshape, ko, vo = _pools(k_out, v_out, (torch.bfloat16, torch.float16, torch.float32))
-    _need(oshape[1:] == shape[1:], "the output pools must have the int8 pools' heads, page size and Dh")
+    dev = _begin(k_pages, "k_pages")
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
+    num_out, dt = k_out.shape[0], k_out.dtype
+    oshape = (num_out, H_kv, P, Dh)
     n = src_pages.numel()
-    rc = lib().kv_dequant_pages_int8(ko, vo, _torch_dtype_code(k_out), oshape[0], kp, vp, sc,
-                                     _ids(src_pages, "src_pages", n, torch.int32), _ids(dst_pages, "dst_pages", n, torch.int32),
-                                     n, H_kv, Dh, P, num_pages, _flag(err_flag), _stream(stream))
+    rc = lib().kv_dequant_pages_int8(
+        _at(k_out, dev, "k_out", oshape, dt), _at(v_out, dev, "v_out", oshape, dt), _torch_dtype_code(k_out), num_out, kp, vp,
+        sc, _at(src_pages, dev, "src_pages", (n,), _torch.int32), _at(dst_pages, dev, "dst_pages", (n,), _torch.int32), n, H_kv,
+        Dh, P, num_pages, _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("kv_dequant_pages_int8", rc)
 
 
 def kv_copy_pages_int8(k_pages, v_pages, kv_scales, src_pages, dst_pages, err_flag=None, stream=None) -> None:
     """kv_copy_pages of int8 pools: codes and scales of pages src_pages[i] -> dst_pages[i] (int32, device)."""
-    import torch
-
-    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    dev = _begin(k_pages, "k_pages")
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
     n = src_pages.numel()
-    rc = lib().kv_copy_pages_int8(kp, vp, sc, _ids(src_pages, "src_pages", n, torch.int32),
-                                  _ids(dst_pages, "dst_pages", n, torch.int32), n, H_kv, Dh, P, num_pages,
-                                  _flag(err_flag), _stream(stream))
+    rc = lib().kv_copy_pages_int8(kp, vp, sc, _at(src_pages, dev, "src_pages", (n,), _torch.int32),
+                                  _at(dst_pages, dev, "dst_pages", (n,), _torch.int32), n, H_kv, Dh, P, num_pages,
+                                  _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("kv_copy_pages_int8", rc)
 
 
@@ -596,16 +616,16 @@ def paged_decode_attention_int8(out, q, k_pages, v_pages, kv_scales, block_table
                                 num_splits: int = 0, workspace=None, err_flag=None, stream=None) -> None:
     """Decode over int8 pools [num_pages, H_kv, P, Dh] with scales [num_pages, H_kv, 2, P]; q bf16/fp16 [B, H_q, Dh];
     other arguments as paged_decode_attention."""
-    import torch
-
-    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools(k_pages, v_pages, kv_scales)
+    dev = _begin(k_pages, "k_pages")
+    (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
     B, H_q, _ = q.shape
-    ws, ws_bytes = _scratch(workspace)
+    mb = block_tables.shape[1]
+    ws, ws_bytes = _scratch_at(workspace, dev)
     rc = lib().paged_decode_attention_int8(
-        _here(out, "out", (B, H_q, Dh), torch.float32), _here(q, "q", (B, H_q, Dh)), _torch_dtype_code(q), kp, vp, sc,
-        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
-        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale), num_splits, ws,
-        ws_bytes, _flag(err_flag), _stream(stream))
+        _at(out, dev, "out", (B, H_q, Dh), _torch.float32), _at(q, dev, "q", (B, H_q, Dh), q.dtype), _torch_dtype_code(q), kp,
+        vp, sc, _at(block_tables, dev, "block_tables", (B, mb), _torch.int32), mb,
+        _at(seq_lens, dev, "seq_lens", (B,), _torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale), num_splits, ws, ws_bytes,
+        _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("paged_decode_attention_int8", rc)
 
 
@@ -614,17 +634,20 @@ def paged_decode_attention_mod(out, q, k_pages, v_pages, block_tables, seq_lens,
                                err_flag=None, stream=None) -> None:
     """paged_decode_attention (bf16/fp16 pools) with capped scores (softcap > 0), a distance bias (alibi_slopes fp32
     [H_q]), a sliding window (window > 0) and a first visible key per sequence (key_start int32 [B])."""
-    import torch
-
-    (num_pages, H_kv, P, Dh), kp, vp = _pools(k_pages, v_pages, (torch.bfloat16, torch.float16, torch.float32))
+    dev = _begin(k_pages, "k_pages")
+    pshape = num_pages, H_kv, P, Dh = k_pages.shape
+    dt, i32 = k_pages.dtype, _torch.int32
     B, H_q, _ = q.shape
-    ws, ws_bytes = _scratch(workspace)
+    mb = block_tables.shape[1]
+    ws, ws_bytes = _scratch_at(workspace, dev)
     rc = lib().paged_decode_attention_mod(
-        _here(out, "out", (B, H_q, Dh), torch.float32), _here(q, "q", (B, H_q, Dh), k_pages.dtype), kp, vp,
-        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
-        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale),
-        _torch_dtype_code(k_pages), float(softcap), _here(alibi_slopes, "alibi_slopes", (H_q,), torch.float32), int(window),
-        _here(key_start, "key_start", (B,), torch.int32), num_splits, ws, ws_bytes, _flag(err_flag), _stream(stream))
+        _at(out, dev, "out", (B, H_q, Dh), _torch.float32), _at(q, dev, "q", (B, H_q, Dh), dt),
+        _at(k_pages, dev, "k_pages", pshape, dt), _at(v_pages, dev, "v_pages", pshape, dt),
+        _at(block_tables, dev, "block_tables", (B, mb), i32), mb, _at(seq_lens, dev, "seq_lens", (B,), i32), B, H_q, H_kv, Dh,
+        P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
+        _at_or_none(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
+        _at_or_none(key_start, dev, "key_start", (B,), i32), num_splits, ws, ws_bytes, _flag_at(err_flag, dev),
+        _raw_stream(stream, dev))
     _check("paged_decode_attention_mod", rc)
 
 
@@ -633,19 +656,19 @@ def paged_prefill_attention_mod(out, q, q_start, max_q_len: int, k_pages, v_page
                                 prefix_lens=None, err_flag=None, stream=None) -> None:
     """paged_prefill_attention with the score and mask options of paged_decode_attention_mod (key_start int32 [N], one
     per row) and a bidirectional prefix per sequence (prefix_lens int32 [B])."""
-    import torch
-
-    (num_pages, H_kv, P, Dh), kp, vp = _pools(k_pages, v_pages, (torch.bfloat16, torch.float16, torch.float32))
+    dev = _begin(k_pages, "k_pages")
+    pshape = num_pages, H_kv, P, Dh = k_pages.shape
+    dt, i32 = k_pages.dtype, _torch.int32
     N, H_q, _ = q.shape
-    B = seq_lens.shape[0]
+    B, mb = block_tables.shape
     rc = lib().paged_prefill_attention_mod(
-        _here(out, "out", (N, H_q, Dh), torch.float32), _here(q, "q", (N, H_q, Dh), k_pages.dtype),
-        _here(q_start, "q_start", (B + 1,), torch.int32), int(max_q_len), kp, vp,
-        _here(block_tables, "block_tables", (B, block_tables.shape[1]), torch.int32), block_tables.shape[1],
-        _here(seq_lens, "seq_lens", (B,), torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale),
-        _torch_dtype_code(k_pages), float(softcap), _here(alibi_slopes, "alibi_slopes", (H_q,), torch.float32), int(window),
-        _here(key_start, "key_start", (N,), torch.int32), _here(prefix_lens, "prefix_lens", (B,), torch.int32),
-        _flag(err_flag), _stream(stream))
+        _at(out, dev, "out", (N, H_q, Dh), _torch.float32), _at(q, dev, "q", (N, H_q, Dh), dt),
+        _at(q_start, dev, "q_start", (B + 1,), i32), int(max_q_len), _at(k_pages, dev, "k_pages", pshape, dt),
+        _at(v_pages, dev, "v_pages", pshape, dt), _at(block_tables, dev, "block_tables", (B, mb), i32), mb,
+        _at(seq_lens, dev, "seq_lens", (B,), i32), B, H_q, H_kv, Dh, P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
+        _at_or_none(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
+        _at_or_none(key_start, dev, "key_start", (N,), i32), _at_or_none(prefix_lens, dev, "prefix_lens", (B,), i32),
+        _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("paged_prefill_attention_mod", rc)
 
 
