@@ -452,15 +452,24 @@ int kv_copy_pages_int8(void* k_pages, void* v_pages, float* kv_scales, const int
  * q_dtype (KV_DTYPE_BF16 or KV_DTYPE_F16, any finite values). Warp-MMA kernel
  * only, whatever paged_decode_set_kernel selects (H_q / H_kv <= 64, Dh in
  * {64, 128}, page_size in {16, 32}, num_pages * H_kv * page_size < 2^31);
- * num_splits, workspace and errors as paged_decode_attention, the automatic
- * split count that of E4M3 pools. A block-table entry outside the pool skips
- * that page only. NaN scales of visible tokens give NaN rows; codes and scales
+ * errors as paged_decode_attention. num_splits > 0: that many ranges per row,
+ * merged by a second kernel; 0: persistent CTAs that share the batch's pages
+ * equally (B <= 1024; a split by the host's rule above), rows cut between them
+ * merged by a second kernel; no second kernel where no row can be longer than
+ * 256 tokens. workspace: paged_decode_ext_workspace_bytes. A block-table entry
+ * outside the pool skips that page only. NaN scales of visible tokens give NaN rows; codes and scales
  * behind a sequence's length are never used. */
 int paged_decode_attention_int8(float* out, const void* q, int32_t q_dtype, const void* k_pages, const void* v_pages,
                                 const float* kv_scales, const int32_t* block_tables, int32_t max_blocks,
                                 const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
                                 int32_t page_size, int32_t num_pages, float scale, int32_t num_splits, void* workspace,
                                 size_t ws_bytes, int* err_flag, void* stream);
+
+/* Workspace bytes of paged_decode_attention_int8 and paged_decode_attention_mod
+ * for these arguments (any window; 0 when no partials are left). KV_ERR_ARG for
+ * bad shapes. */
+int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks,
+                                     int32_t page_size, int32_t num_splits, size_t* out);
 
 /* ---- modified scores and masks ------------------------------------------
  * paged_decode_attention and paged_prefill_attention for models whose
@@ -486,10 +495,9 @@ int paged_decode_attention_int8(float* out, const void* q, int32_t q_dtype, cons
  * num_pages * H_kv * page_size < 2^31. */
 
 /* Single-token form: pos = seq_lens[b] - 1. Warp-MMA kernel, whatever
- * paged_decode_set_kernel selects; num_splits, workspace (the bytes that
- * paged_decode_workspace_bytes gives for the same arguments) and errors as
- * paged_decode_attention. With a window the automatic split counts the pages
- * that a window can touch. */
+ * paged_decode_set_kernel selects; errors as paged_decode_attention,
+ * num_splits and workspace as paged_decode_attention_int8 (a window counts as
+ * the pages that it can touch). */
 int paged_decode_attention_mod(float* out, const void* q, const void* k_pages, const void* v_pages,
                                const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens, int32_t B,
                                int32_t H_q, int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, float scale,

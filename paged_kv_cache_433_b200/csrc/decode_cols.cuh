@@ -24,11 +24,21 @@
 // The row maximum is only voted on (any score above the reference by more than
 // 2^8?); the lanes of a head meet in shuffles when it has to move.
 //
+// Work: pieces of (sequence, KV head) rows. With explicit splits a CTA has one
+// piece, given by the grid. Otherwise the launch is balanced: every CTA reads
+// the lengths, lays the rows end to end -- each counted with a few pages more
+// for its fixed cost -- and takes an equal range of that line (the plan of
+// plan_kernel.cuh's stream form, computed by every CTA for itself: no launch
+// before this one; B up to kColsMaxB). The CTAs are as many as fit the machine
+// and walk their range piece by piece, the producer running ahead of the
+// consumers into the next piece. A row cut between CTAs leaves partials in two
+// slots per CTA, which paged_combine_cols_kernel merges.
+//
 // Data movement as in decode_mma.cuh: one producer warp, 2-D TMA boxes of a
 // page's rows x 128 bytes with 128-byte swizzle (64 for int8 rows of 64
-// bytes), a ring of stages; int8 scales are one bulk copy per (page, head).
-// Pages outside the pool are skipped one by one (KV_DEV_ERR_PAGE_RANGE).
-// Bound by HBM where the batch fills the machine.
+// bytes; at most 16 rows for 16-bit pages), a ring of stages; int8 scales are
+// one bulk copy per (page, head). Pages outside the pool are skipped one by
+// one (KV_DEV_ERR_PAGE_RANGE). Bound by HBM where the batch fills the machine.
 #pragma once
 
 #include <cuda.h>
@@ -41,36 +51,46 @@
 
 namespace kvp {
 
-template <int KT, int DH, int P, int NT>
+constexpr int kColsMaxB = 1024;      // sequences of a balanced launch
+constexpr int kColsItemTokens = 64;  // a row's fixed cost in tokens (its queries, its merge)
+constexpr int kColsMinTokens = 128;  // at least one stage per consumer warp and CTA
+
+template <int KT, int DH, int P, int NT, bool DUP>
 struct ColsCfg {
     static constexpr bool kI8 = KT == KV_DTYPE_INT8;
     static constexpr int kEB = kI8 ? 1 : 2;
-    static constexpr int kTP = 32;                               // tokens per stage
-    static constexpr int kPPS = kTP / P;                         // pages per stage
+    static constexpr int kTP = kI8 ? 32 : 16;                    // tokens per stage
+    static constexpr int kU = P < kTP ? P : kTP;                 // rows of a TMA box: a page, or half a page of 32
+    static constexpr int kUPS = kTP / kU;                        // boxes of rows per stage
+    static constexpr int kUPP = P / kU;                          // and per page
     static constexpr int kRowB = DH * kEB;                       // bytes per token row
     static constexpr int kBoxInner = kRowB < 128 ? kRowB : 128;  // bytes per box row
     static constexpr int kBoxes = kRowB / kBoxInner;             // boxes per token row
     static constexpr int kBoxElems = kBoxInner / kEB;
-    static constexpr int kPageB = P * kBoxInner;                 // one page's rows of one box column
+    static constexpr int kUnitB = kU * kBoxInner;                // one box
     static constexpr int kBoxB = kTP * kBoxInner;                // one box column of a stage
     static constexpr int kChunk = kTP * kRowB;                   // K (or V) of one stage
     static constexpr int kStage = 2 * kChunk;
     static constexpr int kScaleB = kI8 ? P * 8 : 0;              // scales of one (page, head): K's P, then V's
     static constexpr int kNC = 4;                                // consumer warps
     static constexpr int kCtas = NT == 1 ? 3 : 2;                // CTAs per SM
-    static constexpr int kBudget = (NT == 1 ? 64 : 96) * 1024;   // ring bytes
-    static constexpr int kNS0 = kBudget / kStage / kNC * kNC;
-    static constexpr int kNS = kNS0 > 16 ? 16 : kNS0;            // stages: a multiple of the consumer warps
-    static constexpr int kMergeB = kNC * NT * 8 * (DH + 2) * 4;  // per-warp (O, m, l) rows, aliased on the ring
-    static constexpr int kRing = kNS * kStage;
-    static constexpr int kOffBars = kRing > kMergeB ? kRing : kMergeB;
-    static constexpr int kOffPages = kOffBars + 16 * kNS;        // bit j of word s: page j of stage s was loaded
-    static constexpr int kOffScales = (kOffPages + 4 * kNS + 127) / 128 * 128;
-    static constexpr int kSmem = 1024 + kOffScales + kNS * kPPS * kScaleB;  // + slack to align the ring to 1024 bytes
+    // a warp's (O, m, l) fragments on their way to the warp that merges: [registers][lanes]
+    static constexpr int kRegs = NT * (DH / 16) * 4 + 4 * NT;
+    static constexpr int kMergeWarp = kRegs * (DUP ? 16 : 32) * 4;
+    static constexpr int kMergeB = (kNC - 1) * kMergeWarp;
+    static constexpr int kFixed = 1024 /* alignment */ + 1024 /* reserved */ + kMergeB + 4 * (kColsMaxB + 1) + 256;
+    static constexpr int kNS0 = (227 * 1024 / kCtas - kFixed) / (kStage + kUPS * kScaleB + 20);
+    static constexpr int kNS = kNS0 > 16 ? 16 : kNS0;            // stages
+    static constexpr int kOffMerge = kNS * kStage;
+    static constexpr int kOffScales = (kOffMerge + kMergeB + 127) / 128 * 128;
+    static constexpr int kOffBars = kOffScales + kNS * kUPS * kScaleB;
+    static constexpr int kOffPages = kOffBars + 16 * kNS;        // bit j of word s: unit j of stage s was loaded
+    static constexpr int kOffPre = kOffPages + 4 * kNS;          // balanced launch: prefix of the rows' spans
+    static constexpr int kSmem = 1024 + kOffPre + 4 * (kColsMaxB + 1) + 4 * 8;
     static constexpr int kThreads = 32 * (kNC + 1);
-    static_assert(kTP % P == 0 && (kBoxInner == 128 || kBoxInner == 64), "shape");
-    static_assert(kNS >= kNC && kNS % kNC == 0, "every stage goes to the same warp each time");
-    static_assert(kSmem * kCtas <= 227 * 1024, "shared memory");
+    static_assert(P % kU == 0 && (kBoxInner == 128 || kBoxInner == 64), "shape");
+    static_assert(kNS >= kNC, "a stage per consumer warp");
+    static_assert((kSmem + 1024) * kCtas <= 227 * 1024, "shared memory");
 };
 
 // Transpose of an 8 x 8 matrix of 16-bit values held two to a lane (row lane / 4, columns 2 (lane % 4), + 1).
@@ -80,15 +100,75 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return r;
 }
 
+// One piece of a row: pages [page0, page0 + n) of (b, kvh); slot < 0: the whole row (its output is written), else the
+// partial slot it leaves.
+struct ColsPiece {
+    int b, kvh, page0, n, len, key_begin, slot;
+    __device__ __forceinline__ int tokens(int P) const { return n > 0 ? min(len - page0 * P, n * P) : 0; }
+};
+
+// Walks a CTA's pieces; every warp of the CTA runs one in step (all values are uniform over the warp).
+template <int P, bool MOD>
+struct ColsWalk {
+    const DecodeParams& p;
+    const int* pre;  // shared: exclusive prefix over b of the row spans D_b (B + 1 entries); nullptr: one grid piece
+    int pos, end;   // line positions (the host keeps the line below 2^31)
+    int start = 0;  // the first one
+    int b, v;
+    bool grid_done = false;
+
+    __device__ __forceinline__ int length(int bb) const {
+        const int len = p.seq_lens[bb];
+        return len < 0 || len > p.max_blocks * P ? 0 : len;
+    }
+    __device__ __forceinline__ int begin_key(int bb, int len) const { return MOD ? min(first_key(p, bb, len - 1), len) : 0; }
+
+    __device__ __forceinline__ bool next(ColsPiece& o) {
+        if (pre == nullptr) {  // (split, kvh, b) of the grid; its slot is set by the caller's row order
+            if (grid_done) return false;
+            grid_done = true;
+            o.b = blockIdx.z;
+            o.kvh = blockIdx.y;
+            o.len = length(o.b);
+            o.key_begin = begin_key(o.b, o.len);
+            const int first0 = o.key_begin / P, n_pages = (o.len + P - 1) / P - first0;
+            const int skip = blockIdx.x * p.pages_per_split;
+            o.page0 = first0 + skip;
+            o.n = p.num_splits > 1 ? min(p.pages_per_split, n_pages - skip) : n_pages;
+            o.slot = p.num_splits > 1 ? 0 : -1;
+            return true;
+        }
+        while (pos < end) {
+            while (pre[b + 1] * p.H_kv <= pos) ++b;
+            const int D = pre[b + 1] - pre[b], local = pos - pre[b] * p.H_kv;
+            const int kvh = local / D, off = local - kvh * D, row_end = pos - off + D;
+            const int take = min(end, row_end) - pos;
+            pos += take;
+            const int p0 = max(off - v, 0), p1 = off + take - v;  // real pages of the row, its span less v
+            if (p1 <= p0) continue;                               // only the fixed cost's part of the span
+            o.b = b;
+            o.kvh = kvh;
+            o.len = length(b);
+            o.key_begin = begin_key(b, o.len);
+            o.page0 = o.key_begin / P + p0;
+            o.n = p1 - p0;
+            const bool whole = p0 == 0 && pos == row_end;
+            o.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (p0 == 0 ? 1 : 0);
+            return true;
+        }
+        return false;
+    }
+};
+
 template <int KT, int QT, int DH, int P, int NT, bool DUP, bool MOD>
-__global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
+__global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT, DUP>::kCtas))
     paged_decode_cols_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                              const __grid_constant__ CUtensorMap tmap_v) {
-    using C = ColsCfg<KT, DH, P, NT>;
+    using C = ColsCfg<KT, DH, P, NT, DUP>;
     constexpr bool kI8 = C::kI8;
     constexpr bool kQBF16 = !kI8 && KT == KV_DTYPE_BF16;  // QK operands: bf16, else f16 (int8 codes are exact in both)
     constexpr bool kPBF16 = kI8 || KT == KV_DTYPE_BF16;   // PV operands (int8: bf16, whose range holds any V scale)
-    constexpr int kTP = C::kTP, kKS = DH / 16, kMT = kTP / 16, kOM = DH / 16, kPPS = C::kPPS;
+    constexpr int kTP = C::kTP, kKS = DH / 16, kMT = kTP / 16, kOM = DH / 16, kUPS = C::kUPS;
     static_assert(!DUP || NT == 1, "doubled columns");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
 
@@ -98,52 +178,13 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);
     }
-    grid_dependency_wait();  // inputs (and a plan) may come from the previous kernel in the stream
-    if (threadIdx.x == 0) grid_launch_dependents();
-
-    // ---- work of this CTA: (split, kvh, b) from the grid, or a planned chunk
-    int split, kvh, b, item = 0, chunk_pages;
-    if (p.items != nullptr) {
-        const int4 it = p.items[blockIdx.x];
-        if (it.x < 0) return;
-        b = it.x;
-        kvh = it.y;
-        split = it.z;
-        item = it.w;
-        chunk_pages = p.plan[0];
-    } else {
-        split = blockIdx.x;
-        kvh = blockIdx.y;
-        b = blockIdx.z;
-        chunk_pages = p.pages_per_split;
-    }
-    const bool chunked = p.items != nullptr || p.num_splits > 1;
-    int len = p.seq_lens[b];
-    if (len < 0 || len > p.max_blocks * P) {
-        if (threadIdx.x == 0 && split == 0 && p.items == nullptr) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
-        len = 0;
-    }
-    // the row's pages are counted from its first visible key
-    const int key_begin = MOD ? first_key(p, b, len - 1) : 0;
-    const int n_pages = (len + P - 1) / P;
-    const int first0 = min(key_begin, len) / P;
-    const int first = first0 + (chunked ? split * chunk_pages : 0);
-    const int n_local = chunked ? min(chunk_pages, n_pages - first) : n_pages - first;
-    const bool split_mode = p.items != nullptr ? n_pages - first0 > chunk_pages : p.num_splits > 1;
-    if (n_local <= 0) {
-        if (!split_mode)
-            for (int e = threadIdx.x; e < p.g * DH; e += blockDim.x)
-                p.out[((int64_t)b * p.H_q + (int64_t)kvh * p.g) * DH + e] = 0.f;
-        return;
-    }
-    const int n_st = (n_local + kPPS - 1) / kPPS;
-
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (sbase - raw);
     const uint32_t full_bar = sbase + C::kOffBars;
     const uint32_t empty_bar = full_bar + 8 * C::kNS;
     volatile int* stage_pages = reinterpret_cast<volatile int*>(smem + C::kOffPages);
+    int* pre = reinterpret_cast<int*>(smem + C::kOffPre);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kNS; ++s) {
             mbar_init(full_bar + 8 * s, 1);
@@ -151,70 +192,157 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
         }
         fence_barrier_init();
     }
-    __syncthreads();
+    grid_dependency_wait();  // the inputs may come from the previous kernel in the stream
+    // Persistent CTAs fill the machine: kernels launched behind them early would take their places (their combine's
+    // CTAs, waiting on SMs that the next launch of this kernel then finds too full: 90 against 70 us a step).
+    if (threadIdx.x == 0 && p.stream_plan == 0) grid_launch_dependents();
 
+    // ---- this CTA's pieces
+    const bool balanced = p.stream_plan != 0;
+    constexpr int v = kColsItemTokens / P;
+    int T = 0, G = 0;
+    ColsWalk<P, MOD> walk{p, balanced ? pre : nullptr, 0, 0, 0, 0, v};
+    if (balanced) {
+        // spans D_b = pages from the first visible key on, plus v (0 without pages), and their prefix: thread t takes
+        // rows t * per .. + per - 1
+        int* warp_sum = pre + kColsMaxB + 1;
+        const int per = (p.B + C::kThreads - 1) / C::kThreads, b0 = threadIdx.x * per;
+        int sum = 0;
+        for (int k = 0; k < per; ++k) {
+            const int bb = b0 + k;
+            if (bb >= p.B) break;
+            const int raw_len = p.seq_lens[bb], len = walk.length(bb);
+            if (raw_len != len && blockIdx.x == 0) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
+            const int n = (len + P - 1) / P - walk.begin_key(bb, len) / P;
+            if (n > 0) sum += n + v;
+            pre[bb + 1] = sum;
+        }
+        int x = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) warp_sum[warp] = x;
+        __syncthreads();
+        int before = x - sum;
+        for (int w = 0; w < warp; ++w) before += warp_sum[w];
+        for (int k = 0; k < per && b0 + k < p.B; ++k) pre[b0 + k + 1] += before;
+        if (threadIdx.x == 0) pre[0] = 0;
+        __syncthreads();
+        for (int bb = blockIdx.x; bb < p.B; bb += gridDim.x)  // rows without a visible page: no piece writes them
+            if (pre[bb + 1] == pre[bb])
+                for (int e = threadIdx.x; e < p.H_q * DH; e += C::kThreads) p.out[(int64_t)bb * p.H_q * DH + e] = 0.f;
+        T = pre[p.B] * p.H_kv;
+        constexpr int kMin = kColsMinTokens / P;
+        G = min(static_cast<int>(gridDim.x), (T + kMin - 1) / kMin);
+        const int c = blockIdx.x;
+        if (c >= G) {
+            if (threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
+            return;
+        }
+        // positions floor(c T / G) .. floor((c + 1) T / G) (without 64-bit divisions: G^2 fits an int)
+        const int whole = T / G, rest = T - whole * G;
+        walk.pos = walk.start = whole * c + rest * c / G;
+        walk.end = whole * (c + 1) + rest * (c + 1) / G;
+        int hi = p.B;  // largest b with H_kv * pre[b] <= pos
+        while (hi - walk.b > 1) {
+            const int mid = (walk.b + hi) >> 1;
+            if (pre[mid] * p.H_kv <= walk.pos) walk.b = mid;
+            else hi = mid;
+        }
+    } else {
+        __syncthreads();
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && walk.length(blockIdx.z) != p.seq_lens[blockIdx.z])
+            raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
+    }
+
+    ColsPiece pc;
+    int gs = 0;  // stages of the pieces before this one
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         // kGrp stages per step: lane l < kGrp claims stage base + l (bounded wait on its empty barrier, expect_tx for
         // its good pages), then every lane issues one TMA box and, for int8, the first lanes one copy of scales each
-        constexpr int kBPS = kPPS * 2 * C::kBoxes;           // boxes per stage
-        constexpr int kGrp = C::kNS >= 16 ? 4 : C::kNS >= 8 ? 2 : 1;  // a group waits for all its stages: at most a quarter of the ring
+        constexpr int kBPS = kUPS * 2 * C::kBoxes;  // boxes per stage
+        constexpr int kGrp = C::kNS >= 16 ? 4 : C::kNS >= 6 ? 2 : 1;  // a group waits for all its stages
+        constexpr int kPPG = kGrp * kUPS / C::kUPP > 0 ? kGrp * kUPS / C::kUPP : 1;  // pages per group (1: or half)
         static_assert(kGrp * kBPS <= 32, "one TMA box per lane");
-        static_assert(32 % (kGrp * kPPS) == 0, "page groups must tile the 32-entry table window");
-        const int32_t* row = p.block_tables + (int64_t)b * p.max_blocks + first;
+        static_assert(32 % kPPG == 0, "page groups must tile the 32-entry table window");
         bool ok = true;
         int issued = 0;
-        int tab = 0;  // block-table entry of page (first page of the group & ~31) + lane
-        for (int base = 0; base < n_st; base += kGrp) {
-            const int pbase = base * kPPS;
-            if ((pbase & 31) == 0) tab = pbase + lane < n_local ? row[pbase + lane] : -1;
-            const int cnt = min(kGrp, n_st - base);
-            int good = 0;
+        while (ok && walk.next(pc)) {
+            const int n_units = (pc.tokens(P) + C::kU - 1) / C::kU, n_st = (n_units + kUPS - 1) / kUPS;
+            const int32_t* row = p.block_tables + (int64_t)pc.b * p.max_blocks + pc.page0;
+            int tab = 0;  // block-table entry of page (first page of the group & ~31) + lane
+            for (int base = 0; base < n_st; base += kGrp) {
+                const int pbase = base * kUPS / C::kUPP;
+                if ((pbase & 31) == 0 && base * kUPS % C::kUPP == 0) tab = pbase + lane < pc.n ? row[pbase + lane] : -1;
+                const int cnt = min(kGrp, n_st - base);
+                int good = 0;
 #pragma unroll
-            for (int j = 0; j < kPPS; ++j) {
-                const int pg = __shfl_sync(0xffffffffu, tab, ((base + lane) * kPPS + j) & 31);
-                const bool here = lane < cnt && (base + lane) * kPPS + j < n_local;
-                const bool in = pg >= 0 && pg < p.num_pages;
-                if (here && !in) raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
-                good |= here && in ? 1 << j : 0;
-            }
-            if (lane < cnt) {
-                const int i = base + lane, s = i % C::kNS;
-                if (i >= C::kNS && !mbar_wait_bounded(empty_bar + 8 * s, ((i / C::kNS) - 1) & 1, kWaitLimitNs)) {
-                    raise_err(p.err, KV_DEV_ERR_TIMEOUT);
-                    ok = false;
-                } else {
-                    stage_pages[s] = good;
-                    if (good)
-                        mbar_arrive_expect_tx(full_bar + 8 * s, __popc(good) * (2 * C::kBoxes * C::kPageB + C::kScaleB));
-                    else
-                        mbar_arrive(full_bar + 8 * s);
+                for (int j = 0; j < kUPS; ++j) {
+                    const int u = (base + lane) * kUPS + j;
+                    const int pg = __shfl_sync(0xffffffffu, tab, (u / C::kUPP) & 31);
+                    const bool here = lane < cnt && u < n_units;
+                    const bool in = pg >= 0 && pg < p.num_pages;
+                    if (here && !in) raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
+                    good |= here && in ? 1 << j : 0;
                 }
-            }
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if constexpr (kI8) {
-                const int st = lane / kPPS, j = lane % kPPS;
+                if (lane < cnt) {
+                    const int i = gs + base + lane, s = i % C::kNS;
+                    if (i >= C::kNS && !mbar_wait_bounded(empty_bar + 8 * s, ((i / C::kNS) - 1) & 1, kWaitLimitNs)) {
+                        raise_err(p.err, KV_DEV_ERR_TIMEOUT);
+                        ok = false;
+                    } else {
+                        stage_pages[s] = good;
+                        if (good)
+                            mbar_arrive_expect_tx(full_bar + 8 * s,
+                                                  __popc(good) * (2 * C::kBoxes * C::kUnitB + C::kScaleB));
+                        else
+                            mbar_arrive(full_bar + 8 * s);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if constexpr (kI8) {  // one page per unit
+                    const int st = lane / kUPS, j = lane % kUPS;
+                    const int g_st = __shfl_sync(0xffffffffu, good, st & 31);
+                    const int pg = __shfl_sync(0xffffffffu, tab, ((base + st) * kUPS + j) & 31);
+                    if (st < cnt && ((g_st >> j) & 1)) {
+                        const int s = (gs + base + st) % C::kNS;
+                        bulk_g2s(sbase + C::kOffScales + (s * kUPS + j) * C::kScaleB,
+                                 p.kv_scales + ((int64_t)pg * p.H_kv + pc.kvh) * (2 * P), C::kScaleB, full_bar + 8 * s);
+                    }
+                }
+                const int st = lane / kBPS, bx = lane % kBPS;
+                const int j = bx / (2 * C::kBoxes);  // unit of the stage
+                const bool is_v = ((bx / C::kBoxes) & 1) != 0;
+                const int bb = bx % C::kBoxes;       // box of the token row
+                const int u = (base + st) * kUPS + j;
                 const int g_st = __shfl_sync(0xffffffffu, good, st & 31);
-                const int pg = __shfl_sync(0xffffffffu, tab, ((base + st) * kPPS + j) & 31);
+                const int pg = __shfl_sync(0xffffffffu, tab, (u / C::kUPP) & 31);
                 if (st < cnt && ((g_st >> j) & 1)) {
-                    const int s = (base + st) % C::kNS;
-                    bulk_g2s(sbase + C::kOffScales + (s * kPPS + j) * C::kScaleB,
-                             p.kv_scales + ((int64_t)pg * p.H_kv + kvh) * (2 * P), C::kScaleB, full_bar + 8 * s);
+                    const int s = (gs + base + st) % C::kNS;
+                    const uint32_t dst = sbase + s * C::kStage + (is_v ? C::kChunk : 0) + bb * C::kBoxB + j * C::kUnitB;
+                    tma_load_2d(dst, is_v ? static_cast<const void*>(&tmap_v) : static_cast<const void*>(&tmap_k),
+                                bb * C::kBoxElems, (pg * p.H_kv + pc.kvh) * P + u % C::kUPP * C::kU, full_bar + 8 * s);
                 }
+                issued = gs + base + cnt;
             }
-            const int st = lane / kBPS, bx = lane % kBPS;
-            const int j = bx / (2 * C::kBoxes);             // page of the stage
-            const bool is_v = ((bx / C::kBoxes) & 1) != 0;
-            const int bb = bx % C::kBoxes;                  // box of the token row
-            const int g_st = __shfl_sync(0xffffffffu, good, st & 31);
-            const int pg = __shfl_sync(0xffffffffu, tab, ((base + st) * kPPS + j) & 31);
-            if (st < cnt && ((g_st >> j) & 1)) {
-                const int s = (base + st) % C::kNS;
-                const uint32_t dst = sbase + s * C::kStage + (is_v ? C::kChunk : 0) + bb * C::kBoxB + j * C::kPageB;
-                tma_load_2d(dst, is_v ? static_cast<const void*>(&tmap_v) : static_cast<const void*>(&tmap_k),
-                            bb * C::kBoxElems, (pg * p.H_kv + kvh) * P, full_bar + 8 * s);
+            gs += n_st;
+        }
+        if (balanced && lane == 0) {
+            // the row that holds this CTA's last position: does it start here (its first real page, that is) and run on?
+            int4 cut = make_int4(-1, 0, 0, 0);
+            const int pos0 = walk.start, last = walk.end - 1;
+            int b = walk.b;  // the walk ended in or before that row's sequence
+            while (pre[b + 1] * p.H_kv <= last) ++b;
+            const int D = pre[b + 1] - pre[b], kvh = (last - pre[b] * p.H_kv) / D, start = pre[b] * p.H_kv + kvh * D;
+            if (walk.end < start + D && walk.end > start + v && pos0 <= start + v) {
+                const int64_t after = static_cast<int64_t>(start) + D;  // the CTA of position after - 1 has the last piece
+                cut = make_int4(b, kvh, static_cast<int>((after * G - 1) / T) - static_cast<int>(blockIdx.x) + 1, 0);
             }
-            issued = base + cnt;
+            p.cuts[blockIdx.x] = cut;
         }
         if (lane == 0)  // every copy has landed before the CTA exits
             for (int i = max(0, issued - C::kNS); i < issued; ++i)
@@ -226,11 +354,22 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
     // -------------------------------------------------------------- consumers
     const int cw = warp - 1;
     const int hs = cw % p.HS;   // slice of 8 NT heads
-    const int wp = cw / p.HS;   // page-warp: stages wp, wp + WP, ...
+    const int wp = cw / p.HS;   // page-warp: every WP-th stage
+    if (wp >= p.WP) return;     // three slices: one warp has no part
     const int r0 = lane >> 2, quad = lane & 3;
     const int heads = min(NT * 8, p.g - hs * NT * 8);  // heads of this slice
+    const uint32_t bar_written = 1 + 2 * hs, bar_free = 2 + 2 * hs;  // named barriers of the slice's warps
+    // fragments of page-warps 1 .. WP - 1 of this slice: [warp][register][lane]
+    constexpr int kLanes = DUP ? 16 : 32;
+    float* merge = reinterpret_cast<float*>(smem + C::kOffMerge) + hs * (p.WP - 1) * (C::kMergeWarp / 4);
+    const int mlane = DUP ? r0 * 2 + (quad & 1) : lane;
+    bool ok = true;
+    for (int piece = 0; walk.next(pc); ++piece) {
+    if (piece > 0 && wp == 0 && p.WP > 1) named_bar_arrive(bar_free, 32 * p.WP);  // the last piece's fragments are read
+    const int n_st = (pc.tokens(P) + kTP - 1) / kTP;
+    const int b = pc.b, kvh = pc.kvh, len = pc.len;
     const int head0 = kvh * p.g + hs * NT * 8;
-
+    const int tok0 = pc.page0 * P;  // first token of the piece
     // Q^T as the B operand: column lane / 4 of column tile nt is head nt * 8 + lane / 4 (DUP: 4 heads twice). 16-bit
     // K/V: k-step kk covers dims kk*16 .. +15; int8: the lane's K words hold dims quad*Dh/4 + 4*kk .. +3.
     uint32_t qb[NT][kKS][2];
@@ -299,24 +438,29 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
         l_part[nt][0] = l_part[nt][1] = 0.f;
     }
 
-    bool ok = true;
-    if (wp < p.WP) {
+    {
         const int mi = lane >> 3, r8 = lane & 7;  // ldmatrix: matrix and row this lane addresses
-        for (int i = wp; i < n_st; i += p.WP) {
-            const int s = i % C::kNS;
-            if (!mbar_wait_bounded(full_bar + 8 * s, (i / C::kNS) & 1, kWaitLimitNs)) {
+        for (int i = (wp + p.WP - gs % p.WP) % p.WP; i < n_st; i += p.WP) {
+            const int gi = gs + i, s = gi % C::kNS;
+            // The ring is not a multiple of the page-warps, so another warp may have the stage's previous use and copies
+            // may land out of order: that use is waited for first (its release), or the parity of the fill could
+            // still be that of two uses ago. The use before it is long released: the producer issues in order and has
+            // issued stage gi - WP of this warp, hence seen the release of gi - WP - kNS >= gi - 2 kNS.
+            if (ok && ((gi >= C::kNS && !mbar_wait_bounded(empty_bar + 8 * s, (gi / C::kNS - 1) & 1, kWaitLimitNs)) ||
+                       !mbar_wait_bounded(full_bar + 8 * s, (gi / C::kNS) & 1, kWaitLimitNs))) {
                 raise_err(p.err, KV_DEV_ERR_TIMEOUT);
-                ok = false;
+                ok = false;  // no stage of this or a later piece any more; the barriers between warps go on
             }
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             const int pages = stage_pages[s];
             const uint32_t sK = sbase + s * C::kStage, sV = sK + C::kChunk;
-            const uint32_t sS = sbase + C::kOffScales + s * (kPPS * C::kScaleB);
-            const int kbase = (first + i * kPPS) * P;
+            const uint32_t sS = sbase + C::kOffScales + s * (kUPS * C::kScaleB);
+            const int kbase = tok0 + i * kTP;
             // visible tokens of the stage: [tlo, thi), on pages that were loaded (the same for every head)
-            const int thi = min(min(kPPS, n_local - i * kPPS) * P, len - kbase);
-            const int tlo = MOD ? key_begin - kbase : 0;
-            const bool whole = tlo <= 0 && thi >= kTP && pages == (1 << kPPS) - 1;
+            const int thi = min(tok0 + pc.n * P, len) - kbase;
+            const int tlo = MOD ? pc.key_begin - kbase : 0;
+            const bool whole = tlo <= 0 && thi >= kTP && pages == (1 << kUPS) - 1;
 
             // ---- S^T = K Q^T: rows r0 / r0 + 8 of token tile mt, columns 2 quad, + 1
             float sc[NT][kMT][4];
@@ -370,7 +514,7 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
                         ks = lds_float(at);
                         vs[mt][h] = lds_float(at + P * 4);
                     }
-                    const bool seen = whole || (t >= tlo && t < thi && ((pages >> (mt * 16 / P)) & 1));
+                    const bool seen = whole || (t >= tlo && t < thi && ((pages >> (mt * 16 / C::kU)) & 1));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -433,7 +577,7 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
                     constexpr int kCPR = 8;  // 16-byte chunks per box row
                     for (int idx = lane; idx < kTP * C::kBoxes * kCPR; idx += 32) {
                         const int t = idx / (C::kBoxes * kCPR), rem = idx % (C::kBoxes * kCPR);
-                        if (t < tlo || t >= thi || !((pages >> (t / P)) & 1))
+                        if (t < tlo || t >= thi || !((pages >> (t / C::kU)) & 1))
                             sts128_zero(sV + (rem / kCPR) * C::kBoxB + t * 128 + ((rem % kCPR) << 4));
                     }
                     fence_proxy_async_smem();
@@ -493,9 +637,10 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
         }
     }
 
-    // ---- finalize: column sums over the lanes of a head, then merge the page-warps in shared memory
-    named_bar_sync(1, 32 * C::kNC);  // every consumer is done with the stages (the merge rows alias them)
-    float* merge = reinterpret_cast<float*>(smem);  // [kNC][8 NT][DH + 2]
+    gs += n_st;
+
+    // ---- column sums over the lanes of a head; the slice's page-warps meet in the first of them
+    float m_col[NT][2], l_col[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -503,50 +648,182 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
             float l = l_part[nt][e];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+            l_col[nt][e] = l;
             // a NaN sum keeps its place in the merge whatever the column's maximum is
-            const float mr = l != l && m_ref[nt][e] == -INFINITY ? 0.f : m_ref[nt][e];
-            const int n = nt * 8 + 2 * quad + e;
-            float* dst = merge + (cw * NT * 8 + n) * (DH + 2);
+            m_col[nt][e] = l != l && m_ref[nt][e] == -INFINITY ? 0.f : m_ref[nt][e];
+            if constexpr (DUP) {  // values and residuals of a head
 #pragma unroll
-            for (int m = 0; m < kOM; ++m)
+                for (int m = 0; m < kOM; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x = o[nt][m][2 * h + e];
-                    if constexpr (DUP) x += __shfl_xor_sync(0xffffffffu, x, 2);  // values and residuals of a head
-                    const int d = kI8 ? r0 * (DH / 8) + 2 * m + h : m * 16 + h * 8 + r0;
-                    if (n < heads && wp < p.WP) dst[d] = x;
-                }
-            if (r0 == 0 && n < heads && wp < p.WP) dst[DH] = mr, dst[DH + 1] = l;
-        }
-    named_bar_sync(1, 32 * C::kNC);
-
-    for (int e = threadIdx.x - 32; e < p.g * DH; e += 32 * C::kNC) {
-        const int hh = e / DH, d = e % DH;
-        const int slice = hh / (NT * 8), n = hh % (NT * 8);
-        float mstar = -INFINITY;
-        for (int w = 0; w < p.WP; ++w) mstar = fmaxf(mstar, merge[((w * p.HS + slice) * NT * 8 + n) * (DH + 2) + DH]);
-        float L = 0.f, U = 0.f;
-        if (mstar != -INFINITY) {
-            for (int w = 0; w < p.WP; ++w) {
-                const float* src = merge + ((w * p.HS + slice) * NT * 8 + n) * (DH + 2);
-                if (src[DH] == -INFINITY) continue;
-                const float sw = exp2f(src[DH] - mstar);
-                L += sw * src[DH + 1];
-                U += sw * src[d];
+                    for (int h = 0; h < 2; ++h)
+                        o[nt][m][2 * h + e] += __shfl_xor_sync(0xffffffffu, o[nt][m][2 * h + e], 2);
             }
         }
-        // An infinity among the visible values meets a probability's residual, which may be 0 or negative: a NaN.
-        // Where a sum is NaN and the weights are not (rare), the values say what it is.
-        if constexpr (MOD)
-            if (U != U && L == L)
-                U = sum_nonfinite<kPBF16>(p, b, kvh, P, DH, d, max(key_begin, first * P), min(len, (first + n_local) * P));
-        const int64_t hq = (int64_t)b * p.H_q + (int64_t)kvh * p.g + hh;
-        if (!split_mode) {
-            p.out[hq * DH + d] = L != 0.f ? U / L : 0.f;
-        } else {
-            const int64_t ps = p.items != nullptr ? (int64_t)item * p.g + hh : hq * p.num_splits + split;
-            p.part_u[ps * DH + d] = U;
-            if (d == 0) p.part_ml[ps] = make_float2(mstar, L);
+    if (wp > 0) {
+        if (piece > 0) named_bar_sync(bar_free, 32 * p.WP);
+        float* dst = merge + (wp - 1) * (C::kMergeWarp / 4) + mlane;
+        if (!DUP || quad < 2) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int m = 0; m < kOM; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[((nt * kOM + m) * 4 + e) * kLanes] = o[nt][m][e];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    dst[(NT * kOM * 4 + nt * 4 + e) * kLanes] = m_col[nt][e];
+                    dst[(NT * kOM * 4 + nt * 4 + 2 + e) * kLanes] = l_col[nt][e];
+                }
+            }
+        }
+        named_bar_arrive(bar_written, 32 * p.WP);
+        continue;
+    }
+    if (p.WP > 1) named_bar_sync(bar_written, 32 * p.WP);
+    for (int w = 0; w < p.WP - 1; ++w) {
+        const float* src = merge + w * (C::kMergeWarp / 4) + mlane;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mw = src[(NT * kOM * 4 + nt * 4 + e) * kLanes];
+                const float lw = src[(NT * kOM * 4 + nt * 4 + 2 + e) * kLanes];
+                if (mw == -INFINITY) continue;
+                const float mn = fmaxf(m_col[nt][e], mw);
+                const float sa = m_col[nt][e] == -INFINITY ? 0.f : exp2f(m_col[nt][e] - mn), sb = exp2f(mw - mn);
+                m_col[nt][e] = mn;
+                l_col[nt][e] = l_col[nt][e] * sa + lw * sb;
+#pragma unroll
+                for (int m = 0; m < kOM; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        o[nt][m][2 * h + e] = o[nt][m][2 * h + e] * sa + src[((nt * kOM + m) * 4 + 2 * h + e) * kLanes] * sb;
+            }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = nt * 8 + 2 * quad + e;
+            if (n >= heads) continue;
+            const int64_t hq = (int64_t)b * p.H_q + head0 + n;
+            const bool whole = pc.slot < 0;
+            const int64_t ps = balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : hq * p.num_splits + blockIdx.x;
+            float* dst = whole ? p.out + hq * DH : p.part_u + ps * DH;
+            const float L = l_col[nt][e], scale = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
+#pragma unroll
+            for (int m = 0; m < kOM; ++m) {
+                float x[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    x[h] = o[nt][m][2 * h + e];
+                    // An infinity among the visible values meets a probability's residual, which may be 0 or negative:
+                    // a NaN. Where a sum is NaN and the weights are not (rare), the values say what it is.
+                    if constexpr (MOD)
+                        if (x[h] != x[h] && L == L)
+                            x[h] = sum_nonfinite<kPBF16>(p, b, kvh, P, DH, m * 16 + h * 8 + r0, max(pc.key_begin, tok0),
+                                                         min(len, tok0 + pc.n * P));
+                    x[h] = whole && L == 0.f ? 0.f : x[h] * scale;
+                }
+                if constexpr (kI8) {
+                    *reinterpret_cast<float2*>(dst + r0 * (DH / 8) + 2 * m) = make_float2(x[0], x[1]);
+                } else {
+                    dst[m * 16 + r0] = x[0];
+                    dst[m * 16 + 8 + r0] = x[1];
+                }
+            }
+            if (!whole && r0 == 0) p.part_ml[ps] = make_float2(m_col[nt][e], L);
+        }
+    }
+}
+
+// Merges the rows that a balanced launch cut: CTA c takes the row that starts in CTA c's range and runs past its end
+// (cuts[c]: sequence, KV head, pieces), whose pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: the
+// warps share out the heads of the row's group and, with fewer heads than warps, a head's pieces (a long row of a small
+// batch is cut into dozens); a lane sums Dh / 32 dims with the loads of a round of pieces issued before any is used,
+// relative to its warp's own maximum, and the warps of a head meet in shared memory.
+constexpr int kCombineColsWarps = 16;
+template <int DH>
+__global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_kernel(
+    float* __restrict__ out, const float* __restrict__ part_u, const float2* __restrict__ part_ml,
+    const int4* __restrict__ cuts, int32_t H_q, int32_t g) {
+    constexpr int kD = DH / 32, kRound = 8;
+    __shared__ float red_u[kCombineColsWarps][DH], red_m[kCombineColsWarps], red_l[kCombineColsWarps];
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_launch_dependents();
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 cut = cuts[c];
+    if (cut.x < 0) return;
+    const int ns = cut.z;
+    const int wph = max(1, kCombineColsWarps / g);  // warps per head
+    auto slot = [&](int s) -> int64_t { return s == 0 ? 2LL * c + 1 : 2LL * (c + s); };
+    for (int h0 = 0; h0 < g; h0 += kCombineColsWarps) {  // one round unless the group has more heads than warps
+        const int h = h0 + warp / wph, part = warp % wph;
+        float m = -INFINITY, L = 0.f, acc[kD] = {};
+        if (h < g) {
+            for (int s0 = part; s0 < ns; s0 += wph * kRound) {
+                float2 ml[kRound];
+                float x[kRound][kD];
+#pragma unroll
+                for (int j = 0; j < kRound; ++j) {
+                    ml[j] = make_float2(-INFINITY, 0.f);
+                    if (s0 + j * wph >= ns) continue;
+                    const int64_t ps = slot(s0 + j * wph) * g + h;
+                    ml[j] = part_ml[ps];
+                    const float* src = part_u + ps * DH + lane * kD;
+                    if constexpr (kD == 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(src);
+                        x[j][0] = t.x, x[j][1] = t.y, x[j][2] = t.z, x[j][3] = t.w;
+                    } else {
+                        const float2 t = *reinterpret_cast<const float2*>(src);
+                        x[j][0] = t.x, x[j][1] = t.y;
+                    }
+                }
+                float mr = m;
+#pragma unroll
+                for (int j = 0; j < kRound; ++j) mr = fmaxf(mr, ml[j].x);
+                if (mr == -INFINITY) continue;
+                const float a = m == -INFINITY ? 0.f : exp2f(m - mr);
+                m = mr;
+                L *= a;
+#pragma unroll
+                for (int i = 0; i < kD; ++i) acc[i] *= a;
+#pragma unroll
+                for (int j = 0; j < kRound; ++j) {
+                    if (ml[j].x == -INFINITY) continue;
+                    const float w = exp2f(ml[j].x - m);
+                    L += w * ml[j].y;
+#pragma unroll
+                    for (int i = 0; i < kD; ++i) acc[i] += w * x[j][i];
+                }
+            }
+        }
+        if (wph > 1) {
+#pragma unroll
+            for (int i = 0; i < kD; ++i) red_u[warp][lane * kD + i] = acc[i];
+            if (lane == 0) red_m[warp] = m, red_l[warp] = L;
+            __syncthreads();
+            if (h < g && part == 0) {
+                float ms = m;
+                for (int w = 1; w < wph; ++w) ms = fmaxf(ms, red_m[warp + w]);
+                const float a = m == -INFINITY ? 0.f : exp2f(m - ms);
+                L *= a;
+#pragma unroll
+                for (int i = 0; i < kD; ++i) acc[i] *= a;
+                for (int w = 1; w < wph; ++w) {
+                    if (red_m[warp + w] == -INFINITY) continue;
+                    const float sw = exp2f(red_m[warp + w] - ms);
+                    L += sw * red_l[warp + w];
+#pragma unroll
+                    for (int i = 0; i < kD; ++i) acc[i] += sw * red_u[warp + w][lane * kD + i];
+                }
+            }
+        }
+        if (h < g && part == 0) {
+            const float inv = L != 0.f ? 1.f / L : 0.f;
+            float* dst = out + ((int64_t)cut.x * H_q + (int64_t)cut.y * g + h) * DH + lane * kD;
+#pragma unroll
+            for (int i = 0; i < kD; ++i) dst[i] = L != 0.f ? acc[i] * inv : 0.f;
         }
     }
 }
@@ -554,7 +831,7 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT>::kCtas))
 // ---- dispatch ---------------------------------------------------------------
 template <int KT, int QT, int DH, int P, int NT, bool DUP, bool MOD>
 cudaError_t launch_cols_inst(DecodeParams p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t st) {
-    using C = ColsCfg<KT, DH, P, NT>;
+    using C = ColsCfg<KT, DH, P, NT, DUP>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "combine_kernel.cuh"
+#include "decode_cols.cuh"
 #include "decode_launch.cuh"
 #include "fp8.cuh"
 #include "kvpaged.h"
@@ -193,6 +194,8 @@ int keep_shared_carveout() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<128, kCombineWarps, true>, a, c);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, 1, true>, a, c);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_kernel<64, kCombineWarps, true>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_cols_kernel<128>, a, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_combine_cols_kernel<64>, a, c);
     if (e != cudaSuccess) return -1;
     done.fetch_or(bit, std::memory_order_acq_rel);
     return 0;
@@ -418,6 +421,58 @@ struct DecodeExtra {
     const int32_t* key_start = nullptr;
 };
 
+// How a launch of the heads-as-columns kernel (decode_cols.cuh) is laid out. num_splits > 0: that many ranges per row.
+// Otherwise balanced over `grid` persistent CTAs (three per SM for groups of at most 8 heads, two above), except where
+// there is nothing to balance: no row can have more than 256 tokens of visible pages (one CTA per row, no second launch),
+// or every 128 tokens of every row can have a CTA of their own in one wave (the grid splits the rows: a step of one
+// sequence with a window of 512 takes 6.8 us that way, 10.2 balanced, whose CTAs first read the lengths and plan). A batch
+// too large for the CTAs' plan takes the grid rule of resolve_splits.
+struct ColsLayout {
+    bool balanced = false;
+    int32_t S = 1, C = 1, grid = 0;
+    size_t ml_off = 0, u_off = 0, bytes = 0;  // balanced: the cuts come first
+};
+
+constexpr int32_t kColsDirectTokens = 256;
+
+int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks, int32_t page_size, int32_t window,
+                int32_t num_splits, int kv_bytes, ColsLayout* out) {
+    ColsLayout L;
+    int32_t nb = max_blocks;  // pages that a row's visible keys can touch
+    if (window > 0)
+        nb = static_cast<int32_t>(std::min<int64_t>(nb, (static_cast<int64_t>(window) + page_size - 2) / page_size + 1));
+    const int64_t g = H_q / H_kv;
+    const int64_t v = kColsItemTokens / page_size, line = B * static_cast<int64_t>(H_kv) * (nb + v);
+    const int64_t min_pages = kColsMinTokens / page_size, chunks = (nb + min_pages - 1) / min_pages;
+    const bool direct = static_cast<int64_t>(nb) * page_size <= kColsDirectTokens;
+    int64_t slots = 0;
+    if (num_splits == 0) {
+        const int sms = sm_count();
+        if (sms <= 0) return KV_ERR_CUDA;
+        slots = static_cast<int64_t>(sms) * (g <= 8 ? 3 : 2);
+    }
+    const bool one_wave = static_cast<int64_t>(B) * H_kv * chunks <= slots;
+    if (num_splits == 0 && !direct && !one_wave && B <= kColsMaxB && line < (1LL << 31)) {
+        L.balanced = true;
+        L.grid = static_cast<int32_t>(std::min<int64_t>(slots, (line + min_pages - 1) / min_pages));
+        L.ml_off = sizeof(int4) * static_cast<size_t>(L.grid);
+        L.u_off = (L.ml_off + sizeof(float2) * 2 * static_cast<size_t>(L.grid) * g + 15) / 16 * 16;
+        L.bytes = L.u_off + sizeof(float) * 2 * static_cast<size_t>(L.grid) * g * Dh;
+    } else {
+        const int rc = resolve_splits(B, H_kv, max_blocks, num_splits, &L.S, &L.C, kv_bytes);
+        if (rc != KV_OK) return rc;
+        if (num_splits == 0 && direct) L.S = 1;
+        else if (num_splits == 0 && one_wave) L.S = static_cast<int32_t>(chunks);
+        L.C = (nb + L.S - 1) / L.S;
+        L.S = (nb + L.C - 1) / L.C;
+        L.bytes = workspace_for(B, H_q, Dh, L.S);
+        L.u_off = 0;
+        L.ml_off = L.bytes - (L.S > 1 ? sizeof(float2) * static_cast<size_t>(B) * H_q * L.S : 0);
+    }
+    *out = L;
+    return KV_OK;
+}
+
 int check_mod(float softcap, int32_t window) {
     return softcap >= 0.f && softcap < 3.0e38f && window >= 0 ? KV_OK : KV_ERR_ARG;  // a NaN fails the comparison
 }
@@ -546,6 +601,17 @@ int paged_decode_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32_t D
     return KV_OK;
 }
 
+int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks,
+                                     int32_t page_size, int32_t num_splits, size_t* out) {
+    if (!out || B < 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || Dh <= 0 || max_blocks <= 0 ||
+        (page_size != 16 && page_size != 32) || num_splits < 0)
+        return KV_ERR_ARG;
+    ColsLayout L;
+    const int rc = cols_layout(B, H_q, H_kv, Dh, max_blocks, page_size, 0, num_splits, 2, &L);
+    if (rc == KV_OK) *out = L.bytes;
+    return rc;
+}
+
 int paged_decode_launch_info(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks, int32_t page_size,
                              int32_t dtype, int32_t num_splits, int32_t* splits, int32_t* kernel) {
     if (!splits || !kernel || B < 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || Dh <= 0 || max_blocks <= 0 ||
@@ -612,21 +678,17 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
     const int kv_bytes = dtype == KV_DTYPE_INT8 ? 1 : elem_bytes(dtype);
     rc = resolve_splits(B, H_kv, max_blocks, num_splits, &S, &C, kv_bytes);
     if (rc != KV_OK) return rc;
-    if (ex.mod && ex.window > 0) {
-        // a window touches at most nb pages of any row: split those (never more splits than without a window, so
-        // that the workspace of the same arguments holds their partials)
-        const int64_t nb64 = (static_cast<int64_t>(ex.window) + page_size - 2) / page_size + 1;
-        if (nb64 < max_blocks) {
-            const int32_t nb = static_cast<int32_t>(nb64), S_all = S;
-            rc = resolve_splits(B, H_kv, nb, num_splits, &S, &C, kv_bytes);
-            if (rc != KV_OK) return rc;
-            C = (nb + std::min(S, S_all) - 1) / std::min(S, S_all);
-            S = (nb + C - 1) / C;
-        }
-    }
     const bool new_op = ex.mod || dtype == KV_DTYPE_INT8;  // on the heads-as-columns kernel (decode_cols.cuh) only
     const bool tc = mma && !new_op && tc_ok(dtype, g, Dh, cos_sin != nullptr, B, H_kv, num_splits);
-    const bool planned = tc ? planned_tc(B, num_splits) : planned_ok(mma, B, H_q, H_kv, num_splits);
+    const bool planned = !new_op && (tc ? planned_tc(B, num_splits) : planned_ok(mma, B, H_q, H_kv, num_splits));
+    ColsLayout cols;
+    if (new_op) {
+        rc = cols_layout(B, H_q, H_kv, Dh, max_blocks, page_size, ex.window, num_splits, kv_bytes, &cols);
+        if (rc != KV_OK) return rc;
+        if (cols.bytes > 0 && (!workspace || ws_bytes < cols.bytes || !aligned16(workspace))) return KV_ERR_WORKSPACE;
+        S = cols.S;
+        C = cols.C;
+    }
 
     DecodeParams p{};
     p.out = out;
@@ -663,7 +725,18 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
     int64_t pgrid = 0;
     const int sms_all = sm_count();
     if (sms_all <= 0 || keep_shared_carveout() != 0) return KV_ERR_CUDA;
-    if (planned && tc) {
+    if (new_op) {
+        char* w = static_cast<char*>(workspace);
+        if (cols.bytes > 0) {
+            p.part_u = reinterpret_cast<float*>(w + cols.u_off);
+            p.part_ml = reinterpret_cast<float2*>(w + cols.ml_off);
+        }
+        if (cols.balanced) {
+            p.stream_plan = 1;
+            p.cuts = reinterpret_cast<int4*>(w);
+            grid = dim3(static_cast<unsigned>(cols.grid), 1, 1);
+        }
+    } else if (planned && tc) {
         // balanced plan: one persistent CTA per SM, each streaming the same number of pages
         pgrid = sms_all;
         const PlannedLayout L = stream_layout(B, H_q, H_kv, Dh, pgrid);
@@ -707,7 +780,7 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         // resident CTAs of the warp-MMA kernel: two per SM
         const int32_t slots = static_cast<int32_t>(2 * sms_all);
         e = launch_pdl(paged_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, seq_lens, B, H_kv, page_size, max_blocks,
-                       slots, static_cast<int32_t>(pgrid), c_floor, plan, items, p.window, p.key_start, err_flag);
+                       slots, static_cast<int32_t>(pgrid), c_floor, plan, items, err_flag);
         if (e != cudaSuccess) return KV_ERR_CUDA;
         grid = dim3(static_cast<unsigned>(pgrid), 1, 1);
     } else if (S > 1) {
@@ -735,8 +808,9 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
     } else if (mma) {
         CUtensorMap tk, tv;
         const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;
-        if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) ||
-            !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
+        const int32_t box_rows = ex.mod ? std::min<int32_t>(page_size, 16) : page_size;
+        if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, box_rows) ||
+            !make_pool_map(&tv, v_pages, dtype, rows, Dh, box_rows))
             return KV_ERR_CUDA;
         e = ex.mod                   ? launch_cols_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
             : dtype == KV_DTYPE_INT8 ? launch_cols_int8(p, tk, tv, q_dtype, Dh, page_size, grid, st)
@@ -758,6 +832,14 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
                                    static_cast<const int32_t*>(p.plan), B, H_q, H_kv)
                       : launch_pdl(paged_combine_stream_kernel<64>, blocks, threads, 0, st, out, p.part_u, p.part_ml,
                                    static_cast<const int32_t*>(p.plan), B, H_q, H_kv);
+        if (e != cudaSuccess) return KV_ERR_CUDA;
+    } else if (cols.balanced) {
+        const dim3 blocks(static_cast<unsigned>(cols.grid)), threads(32 * kCombineColsWarps);
+        auto merge = [&](auto kernel) {
+            return launch_pdl(kernel, blocks, threads, 0, st, out, p.part_u, p.part_ml,
+                              static_cast<const int4*>(p.cuts), H_q, g);
+        };
+        e = Dh == 128 ? merge(paged_combine_cols_kernel<128>) : merge(paged_combine_cols_kernel<64>);
         if (e != cudaSuccess) return KV_ERR_CUDA;
     } else if (planned || S > 1) {
         // one warp per row when a single round of 8 loads per lane covers the splits (and for

@@ -3,9 +3,7 @@
 // grid and the shorter tail chunks from the back, so the hardware block
 // scheduler -- which starts CTAs in index order -- ends on small pieces
 // (the CTAs in between find no work and exit). C is chosen from the actual
-// page counts, which the host does not see (a row's pages are those from its
-// first visible key on: window and key_start, see plan_layout.cuh; all of them
-// with window = 0 and no key_start): every row the same count -> one
+// lengths, which the host does not see: every row the same length -> one
 // wave (chunks ~ `slots`); otherwise about four chunks per resident slot;
 // never below `c_floor` (keeps each chunk's (m, l, u) partial small next to
 // its K/V). One CTA of 1024 threads; each thread keeps its rows' page counts
@@ -64,7 +62,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const int32_t*
                                                                   int32_t H_kv, int32_t P, int32_t max_blocks,
                                                                   int32_t slots, int32_t grid, int32_t c_floor,
                                                                   int32_t* __restrict__ plan, int4* __restrict__ items,
-                                                                  int32_t window, const int32_t* __restrict__ key_start,
                                                                   int* err) {
     __shared__ unsigned long long warp_sums[32];
     __shared__ int s_min, s_max;
@@ -91,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const int32_t*
                 if (err) atomicOr(err, KV_DEV_ERR_SEQ_LEN);
                 len = 0;
             }
-            n[r] = (len + P - 1) / P - min(first_visible_key(len - 1, window, key_start, b), len) / P;
+            n[r] = (len + P - 1) / P;
             local += n[r];
             mn = min(mn, n[r]);
             mx = max(mx, n[r]);

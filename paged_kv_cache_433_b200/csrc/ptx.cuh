@@ -98,7 +98,10 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-
+// Arrive at a named barrier that other threads wait on with named_bar_sync (the same count).
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 
 // 2-D tiled TMA load (no multicast): box at element coordinates (x, y) of the
 // tensor described by `tmap` lands at `dst_smem`; completion as transaction

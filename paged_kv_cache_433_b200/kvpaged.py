@@ -99,6 +99,7 @@ SIGNATURES = [
     ("paged_decode_attention_mod", ctypes.c_int,
      [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32, _vp, _i32,
       _vp, _sz, _vp, _vp]),
+    ("paged_decode_ext_workspace_bytes", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _psz]),
     ("paged_prefill_attention_mod", ctypes.c_int,
      [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32,
       _vp, _vp, _vp, _vp]),
@@ -610,6 +611,15 @@ def kv_copy_pages_int8(k_pages, v_pages, kv_scales, src_pages, dst_pages, err_fl
                                   _at(dst_pages, dev, "dst_pages", (n,), _torch.int32), n, H_kv, Dh, P, num_pages,
                                   _flag_at(err_flag, dev), _raw_stream(stream, dev))
     _check("kv_copy_pages_int8", rc)
+
+
+def paged_decode_ext_workspace_bytes(B: int, H_q: int, H_kv: int, Dh: int, max_blocks: int, page_size: int,
+                                     num_splits: int = 0) -> int:
+    """Workspace bytes of paged_decode_attention_int8 and paged_decode_attention_mod."""
+    out = ctypes.c_size_t()
+    _check("paged_decode_ext_workspace_bytes",
+           lib().paged_decode_ext_workspace_bytes(B, H_q, H_kv, Dh, max_blocks, page_size, num_splits, out))
+    return out.value
 
 
 def paged_decode_attention_int8(out, q, k_pages, v_pages, kv_scales, block_tables, seq_lens, scale: float,

@@ -148,7 +148,7 @@ def _reference(c, rows=None):
 def _decode(c, num_splits=0, err=None, out=None):
     B = len(c["lens"])
     out = torch.full((B, c["H_q"], c["Dh"]), float("nan"), device="cuda") if out is None else out
-    need = K.paged_decode_workspace_bytes(B, c["H_q"], c["H_kv"], c["Dh"], c["tab"].shape[1], c["P"], num_splits)
+    need = K.paged_decode_ext_workspace_bytes(B, c["H_q"], c["H_kv"], c["Dh"], c["tab"].shape[1], c["P"], num_splits)
     ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
     K.paged_decode_attention_int8(out, c["q"], c["kp"], c["vp"], c["sc"], torch.from_numpy(c["tab"]).cuda(),
                                   torch.from_numpy(c["lens"].astype(np.int32)).cuda(), c["scale"], num_splits=num_splits,

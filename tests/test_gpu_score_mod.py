@@ -100,7 +100,7 @@ def _d(a):
 def _decode(c, q, scale, num_splits=0, key_start=None, err=None, **mod):
     B, H_q, Dh = q.shape
     out = torch.full((B, H_q, Dh), float("nan"), device="cuda")
-    need = K.paged_decode_workspace_bytes(B, H_q, c["H_kv"], Dh, c["tab"].shape[1], c["P"], num_splits)
+    need = K.paged_decode_ext_workspace_bytes(B, H_q, c["H_kv"], Dh, c["tab"].shape[1], c["P"], num_splits)
     ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
     K.paged_decode_attention_mod(out, q, c["kp"], c["vp"], torch.from_numpy(c["tab"]).cuda(), _d(c["lens"]), scale,
                                  num_splits=num_splits, workspace=ws, err_flag=err, key_start=_d(key_start), **mod)
@@ -353,7 +353,7 @@ def test_mod_layer_run():
     d_tab = torch.from_numpy(tab).cuda()
     d_q = torch.empty((1, H_q, Dh), dtype=torch.bfloat16, device="cuda")
     out = torch.empty((1, H_q, Dh), device="cuda")
-    ws = torch.empty(max(16, K.paged_decode_workspace_bytes(1, H_q, H_kv, Dh, 8, P)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(16, K.paged_decode_ext_workspace_bytes(1, H_q, H_kv, Dh, 8, P)), dtype=torch.uint8, device="cuda")
     d_slot.fill_(-1)
     graph = torch.cuda.CUDAGraph()
     side = torch.cuda.Stream()
