@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT, DUP>::kCtas))
             // ---- scores in log2 units, masked; has any moved above the reference by more than 2^8?
             float vs[kMT][2];  // int8: V scales of tokens r0, r0 + 8
             bool grow = false;
-            if constexpr (MOD) modify_cols<NT, kMT>(p, sc, slope, len - 1 - kbase - r0);
+            if constexpr (MOD) modify_cols<NT, kMT>(p, cap_coefs(p), sc, slope, len - 1 - kbase - r0);
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll

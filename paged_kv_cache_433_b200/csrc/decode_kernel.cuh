@@ -81,6 +81,8 @@ struct DecodeParams {
     float cap_in, cap_out;      // tanh cap c (cap_out = 0: none): scale / c and c * log2(e)
     float cap_small;            // products up to this magnitude take the polynomial (negative: none does)
     float cap_coef[6];          // its coefficients
+    float cap_tiny, cap_coef_tiny[3];  // the same of the shorter polynomial for smaller products
+    float fixed_ref;            // chunked prefill, capped bf16: the softmax reference of every row (log2 units)
     const float* alibi_slopes;  // [H_q] (nullable): bias -slope * |query position - key position|
     const int32_t* key_start;   // first visible key per query row (nullable)
     const int32_t* prefix_lens; // multi-token query: keys visible to every row of sequence b (nullable)

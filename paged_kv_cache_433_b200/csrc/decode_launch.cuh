@@ -162,9 +162,9 @@ cudaError_t launch_cols_int8(const DecodeParams& p, const CUtensorMap& tk, const
                              int P, dim3 grid, cudaStream_t st);
 cudaError_t launch_cols_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH, int P,
                             dim3 grid, cudaStream_t st);
-// Multi-token query with modified scores and masks (prefill_mma_mod.cu, prefill_tc_mod.cu).
+// Multi-token query with modified scores and masks (prefill_mma_mod.cu, prefill_mod_tc.cu).
 cudaError_t launch_prefill_tc_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int P,
-                                  dim3 grid, cudaStream_t st);
+                                  bool fixed_ref, dim3 grid, cudaStream_t st);
 cudaError_t launch_prefill_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH,
                                int P, dim3 grid, cudaStream_t st);
 

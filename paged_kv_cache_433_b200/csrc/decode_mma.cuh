@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                     const int kbase = (first + i * PPS) * P;
                     tlo[0] = key_lo[0] - kbase;
                     tlo[1] = key_lo[1] - kbase;
-                    modify_rows<C::kNT>(p, sc, slope, qpos[0] - kbase - 2 * quad, qpos[1] - kbase - 2 * quad);
+                    modify_rows<C::kNT>(p, cap_coefs(p), sc, slope, qpos[0] - kbase - 2 * quad, qpos[1] - kbase - 2 * quad);
                 }
 #pragma unroll
                 for (int n = 0; n < C::kNT; ++n)

@@ -489,7 +489,11 @@ void set_mod(DecodeParams& p, float scale, float softcap, const float* alibi_slo
         p.cap_coef[i] = static_cast<float>(kTanhPoly[i] * f);
         top = std::max(top, std::abs(kTanhPoly[i] * f));
     }
-    p.cap_small = u != 0. && top < 1e30 && kTanhSmall / std::abs(u) < 1e15 ? static_cast<float>(kTanhSmall / std::abs(u)) : -1.f;
+    const bool poly = u != 0. && top < 1e30 && kTanhSmall / std::abs(u) < 1e15;
+    p.cap_small = poly ? static_cast<float>(kTanhSmall / std::abs(u)) : -1.f;
+    p.cap_tiny = poly ? static_cast<float>(kTanhTiny / std::abs(u)) : -1.f;
+    f = o;
+    for (int i = 0; i < kCapTinyTerms; ++i, f *= u * u) p.cap_coef_tiny[i] = static_cast<float>(kTanhTinyPoly[i] * f);
     p.alibi_slopes = alibi_slopes;
     p.window = window;
     p.key_start = key_start;
@@ -1008,9 +1012,14 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     p.scale_log2 = scale * kLog2e;
     p.q_start = q_start;
     p.q_tile = q_tile;
+    bool fixed_ref = false;
     if (mod) {
         set_mod(p, scale, mod->softcap, mod->alibi_slopes, mod->window, mod->key_start);
         p.prefix_lens = mod->prefix_lens;
+        // A cap bounds every score by cap_out; where 2^(2 cap_out) fits fp32's range with room for sums (bf16 operands
+        // have that range too) and no bias moves the scores, one reference serves all rows: no row maximum is taken.
+        fixed_ref = dtype == KV_DTYPE_BF16 && mod->softcap > 0.f && p.cap_out <= kFixedRefMax && !mod->alibi_slopes;
+        p.fixed_ref = std::max(0.f, p.cap_out - 40.f);
     }
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;
@@ -1020,7 +1029,7 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
                     static_cast<unsigned>(B));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
-                          : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, grid, st)
+                          : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, fixed_ref, grid, st)
                           : tc                     ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
                           : dtype == KV_DTYPE_BF16 ? launch_prefill_bf16(p, tk, tv, Dh, page_size, grid, st)
                                                    : launch_prefill_f16(p, tk, tv, Dh, page_size, grid, st);

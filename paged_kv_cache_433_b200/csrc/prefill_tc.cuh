@@ -46,24 +46,11 @@
 // Every wait is bounded (KV_DEV_ERR_TIMEOUT); block-table entries outside
 // [0, num_pages) are never loaded (their keys are masked,
 // KV_DEV_ERR_PAGE_RANGE).
-//
-// MOD instances (score_mod.cuh: tanh cap, distance bias, window, documents,
-// bidirectional prefix): a row sees keys [lo, hi); the tile's stages run from
-// the one that holds the first key any of its rows sees; scores are modified
-// in registers between the load of S and the maximum. A stage that some rows
-// see only in part ("boundary") has its V rows searched for NaN and infinity,
-// which a probability of 0 would not keep from the rows that do not see them:
-// found elements are zeroed in shared memory, and the epilogue of such a tile
-// adds them, read again from the pool, to the rows that do.
 #pragma once
 
 #include <cuda.h>
 
-#include <atomic>
-
 #include "decode_kernel.cuh"
-#include "decode_launch.cuh"
-#include "score_mod.cuh"
 #include "tc05.cuh"
 
 namespace kvp {
@@ -86,7 +73,6 @@ struct PfCfg {
     // full[R], empty[R], q_full, s_full[3], p_full[3], p_empty[3], o_full, done (QK), done (PV)
     static constexpr int kNumBars = 2 * kRing + 1 + 3 + 3 + 3 + 3;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
-    static constexpr int kOffDirty = kOffTmem + 8;  // MOD: a boundary stage held a NaN or an infinity in V
     static constexpr int kSmem = 1024 + kOffTmem + 16;
     static constexpr int kThreads = 384;
     static constexpr int kVWarp = 2;             // the V producer (warp 0 produces K)
@@ -103,22 +89,7 @@ struct PfCfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// row[0..31] = row * scale (if `more`) + a: accumulator columns onto the sums that an output row holds.
-__device__ __forceinline__ void add_to_row(float* row, const uint32_t (&a)[32], float scale, bool more) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        float4* at = reinterpret_cast<float4*>(row + i);
-        float4 v = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]), __uint_as_float(a[i + 2]),
-                               __uint_as_float(a[i + 3]));
-        if (more) {
-            const float4 o = *at;
-            v = make_float4(fmaf(o.x, scale, v.x), fmaf(o.y, scale, v.y), fmaf(o.z, scale, v.z), fmaf(o.w, scale, v.w));
-        }
-        *at = v;
-    }
-}
-
-template <int KT, int DH, int P, bool MOD = false>
+template <int KT, int DH, int P>
 __global__ void __launch_bounds__(384, 1)
     paged_prefill_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v) {
@@ -126,7 +97,6 @@ __global__ void __launch_bounds__(384, 1)
     constexpr bool kBF16 = KT == KV_DTYPE_BF16;
     constexpr uint32_t kIdescQK = idesc_f16(kBF16, 128, C::kTP, false, false);
     constexpr uint32_t kIdescPV = idesc_f16(kBF16, 128, DH, false, true);
-    constexpr int kFlush = kFlushKeys / C::kTP;  // MOD: stages whose P.V share one accumulation
     extern __shared__ __align__(1024) unsigned char smem_raw[];
 
     const int warp = threadIdx.x >> 5;
@@ -147,37 +117,19 @@ __global__ void __launch_bounds__(384, 1)
     if (t0 >= n_q) return;
     const int nt = min(p.q_tile, n_q - t0);
     int len = p.seq_lens[b];
-    auto zero_tile = [&]() {
+    if (len < 0 || len > p.max_blocks * P || n_q > len) {
+        if (threadIdx.x == 0 && t0 == 0 && kvh == 0) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
+        // rows of this tile are zero
         for (int e = threadIdx.x; e < nt * g * DH; e += blockDim.x) {
             const int rr = e / DH;
             p.out[((int64_t)(qs0 + t0 + rr / g) * p.H_q + (int64_t)kvh * g + rr % g) * DH + e % DH] = 0.f;
         }
-    };
-    if (len < 0 || len > p.max_blocks * P || n_q > len) {
-        if (threadIdx.x == 0 && t0 == 0 && kvh == 0) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
-        zero_tile();
         return;
     }
     const int pos0 = len - n_q + t0;          // position of the tile's first token
-    // some row sees keys in [key_begin, key_end) only; all rows see every key of [key_all0, key_all1)
-    int key_begin = 0, key_end = pos0 + nt, key_all0 = 0, key_all1 = pos0 + 1, prefix = 0;
-    if constexpr (MOD) {
-        prefix = p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0;
-        const TileKeys tk = tile_keys(p, qs0 + t0, pos0, nt, prefix, lane);
-        key_begin = tk.begin;
-        key_end = tk.end;
-        key_all0 = tk.all0;
-        key_all1 = tk.all1;
-        if (key_begin >= key_end) {  // no row sees any key
-            zero_tile();
-            return;
-        }
-    }
-    // stages, pages and keys are counted from the first stage with a visible key
-    const int key_first = MOD ? key_begin / C::kTP * C::kTP : 0;
-    const int page_first = key_first / P;
-    const int n_pages = (key_end + P - 1) / P - page_first;
-    const int n_st = (key_end - key_first + C::kTP - 1) / C::kTP;
+    const int key_end = pos0 + nt;            // keys 0 .. key_end - 1 are seen by some row
+    const int n_pages = (key_end + P - 1) / P;
+    const int n_st = (key_end + C::kTP - 1) / C::kTP;
 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -216,7 +168,6 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(o_full, 1);
         mbar_init(done_qk, 1);
         mbar_init(done_pv, 1);
-        if (MOD) *reinterpret_cast<volatile int*>(smem + C::kOffDirty) = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -241,7 +192,7 @@ __global__ void __launch_bounds__(384, 1)
         const int half = warp == 0 ? 0 : 1;
         bool ok = true;
         int kfills = 0, vfills = 0;  // stages whose K / V boxes were issued
-        const int32_t* row = p.block_tables + (int64_t)b * p.max_blocks + page_first;
+        const int32_t* row = p.block_tables + (int64_t)b * p.max_blocks;
         int tab_cur = lane < n_pages ? row[lane] : -1, tab_nxt = -1;
         for (int j = 0; j < n_st && ok; ++j) {
             const int np = min(C::kPPS, n_pages - j * C::kPPS);
@@ -336,7 +287,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
                         umma_ts(tO, tP + kk * 8, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128), kIdescPV,
-                                ((MOD ? j % kFlush != 0 : j > 0) || kk > 0) ? 1u : 0u);
+                                (j > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
                         umma_ts(tO, tP + C::kTP / 2 + kk * 8, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128),
@@ -362,14 +313,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t pair_bar = 1 + quarter;  // named barrier of the two warps that share row r
         const int tr = r / g;
         const bool row_valid = tr < nt;
-        const int pos = pos0 + tr;           // this row sees keys 0 .. pos (MOD: row_lo .. row_hi - 1)
-        int row_lo = 0, row_hi = pos + 1;
-        float slope = 0.f;
-        if (MOD && row_valid) {
-            row_lo = first_key(p, qs0 + t0 + tr, pos);
-            row_hi = max(pos + 1, prefix);
-            if (p.alibi_slopes != nullptr) slope = p.alibi_slopes[kvh * g + r % g] * kLog2e;
-        }
+        const int pos = pos0 + tr;           // this row sees keys 0 .. pos
         const int64_t qrow = ((int64_t)(qs0 + t0 + tr) * p.H_q + (int64_t)kvh * g + r % g);
         float* xm = reinterpret_cast<float*>(smem + C::kOffX);        // [buf][half][row] partial maxima / sums
         int* xok = reinterpret_cast<int*>(smem + C::kOffX) + 2 * 2 * 128;
@@ -412,11 +356,10 @@ __global__ void __launch_bounds__(384, 1)
         };
         const float sl2 = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
-        float sum_scale = 1.f;  // MOD: the factor from the sums kept in the output row to the current reference
         constexpr int kH = C::kTP / 2;       // key columns per thread
         // lanes 0 .. kPPS-1: the page ids of stage j, read one stage ahead; the mask of pages the producers
         // skip (entries outside the pool) is then known without waiting for the V entry
-        const int32_t* trow = p.block_tables + (int64_t)b * p.max_blocks + page_first;
+        const int32_t* trow = p.block_tables + (int64_t)b * p.max_blocks;
         int pg_cur = lane < C::kPPS && lane < n_pages ? __ldg(trow + lane) : -1;
         for (int j = 0; j < n_st; ++j) {
             bool okl = ok;
@@ -435,21 +378,19 @@ __global__ void __launch_bounds__(384, 1)
             }
             // keys of this stage: kbase .. kbase + 127; the V entry carries the skipped-page mask
             const int ev = vslot(j);
-            const int kbase = key_first + j * C::kTP;
+            const int kbase = j * C::kTP;
             const int np = min(C::kPPS, n_pages - j * C::kPPS);
             const unsigned loaded = __ballot_sync(0xffffffffu, lane < np && pg_cur >= 0 && pg_cur < p.num_pages);
             const int bad = static_cast<int>(~loaded & ((1u << np) - 1u));
             pg_cur = pg_nxt;
             // keys this row may see in the stage: [0, lim); pages skipped or not loaded are masked
-            const int lim = row_valid ? min(C::kTP, row_hi - kbase) : 0;
-            const int low = MOD ? row_lo - kbase : 0;
-            const bool full_stage = lim == C::kTP && np == C::kPPS && bad == 0 && low <= 0;
-            if constexpr (MOD) modify_row(p, s, slope, pos - kbase - half * kH);
+            const int lim = row_valid ? min(C::kTP, pos + 1 - kbase) : 0;
+            const bool full_stage = lim == C::kTP && np == C::kPPS && bad == 0;
             if (!full_stage || !okl) {
 #pragma unroll
                 for (int c = 0; c < kH; ++c) {
                     const int cc = half * kH + c, pgi = cc / P;
-                    if (!okl || cc >= lim || cc < low || pgi >= np || ((bad >> pgi) & 1)) s[c] = -INFINITY;
+                    if (!okl || cc >= lim || pgi >= np || ((bad >> pgi) & 1)) s[c] = -INFINITY;
                 }
             }
             float mx = -INFINITY;
@@ -460,7 +401,7 @@ __global__ void __launch_bounds__(384, 1)
                 ok = false;  // both halves of every row of this pair stop here
                 break;
             }
-            const float mx2 = MOD ? mx : mx * sl2;  // sl2 > 0: the scaled maximum of the whole row
+            const float mx2 = mx * sl2;  // sl2 > 0: the scaled maximum of the whole row
             // reference maximum: moves only when the row's max exceeds it by more than 2^8
             const bool need = mx2 > m_ref + 8.f;
             float alpha = 1.f;
@@ -469,8 +410,7 @@ __global__ void __launch_bounds__(384, 1)
                 m_ref = mx2;
                 l *= alpha;
             }
-            const bool flush = MOD && j > 0 && j % kFlush == 0;
-            if (flush || (j > 0 && __any_sync(0xffffffffu, need))) {
+            if (j > 0 && __any_sync(0xffffffffu, need)) {
                 // O holds P.V of the earlier stages: wait for the last one, then rescale this half of the rows
                 if (!wait(okl, p_empty((j - 1) % 3), ((j - 1) / 3) & 1)) {
                     ok = false;  // the next meeting stops the pair
@@ -483,19 +423,12 @@ __global__ void __launch_bounds__(384, 1)
                     uint32_t a[32];
                     tmem_ld32(tO + lane_addr + half * kH + q2 * 32, a);
                     tmem_wait_ld();
-                    if (flush) {  // P.V of this stage starts a new accumulation
-                        if (row_valid)
-                            add_to_row(p.out + qrow * DH + half * kH + q2 * 32, a, sum_scale, j > kFlush);
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * alpha);
-                        tmem_st32(tO + lane_addr + half * kH + q2 * 32, a);
-                    }
+                    for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * alpha);
+                    tmem_st32(tO + lane_addr + half * kH + q2 * 32, a);
                 }
                 tmem_wait_st();
-                if (flush) sum_scale = 1.f;
             }
-            if (MOD) sum_scale *= alpha;
             // probabilities -> P over this S buffer: hi pairs in columns 0..63, residual pairs in 64..127
             // (this thread's keys: hi columns 32 half .., lo columns 64 + 32 half ..)
             const float neg = (m_ref == -INFINITY) ? 0.f : -m_ref;
@@ -507,14 +440,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     // two keys at a time: one packed multiply-add for the exponents, one packed add for the sums
-                    const float2 sv = make_float2(s[q2 * 32 + 2 * i], s[q2 * 32 + 2 * i + 1]);
-                    const float2 x = MOD ? fadd2(sv, negv) : ffma2(sv, sl2v, negv);
+                    const float2 x = ffma2(make_float2(s[q2 * 32 + 2 * i], s[q2 * 32 + 2 * i + 1]), sl2v, negv);
                     const float p0 = exp2f(x.x), p1 = exp2f(x.y);  // exp2(-inf) = 0 for masked keys
                     lsum = fadd2(lsum, make_float2(p0, p1));
-                    if constexpr (MOD)
-                        pack2_split_near<kBF16>(p0, p1, hi[i], lo[i]);
-                    else
-                        pack2_split_fast<kBF16>(p0, p1, hi[i], lo[i]);
+                    pack2_split_fast<kBF16>(p0, p1, hi[i], lo[i]);
                 }
                 tmem_st16(tmem + (j % 3) * C::kTP + lane_addr + half * 32 + q2 * 16, hi);
                 tmem_st16(tmem + (j % 3) * C::kTP + lane_addr + C::kTP / 2 + half * 32 + q2 * 16, lo);
@@ -526,10 +455,8 @@ __global__ void __launch_bounds__(384, 1)
             // row wait for it (the P.V issuer waits for every entry)
             {
                 const int pgi = r / P;
-                const bool stale = kbase + r >= key_end || kbase + r < key_begin || pgi >= np || ((bad >> pgi) & 1);
-                // MOD: a key that some rows of the tile do not see must not reach them as 0 times NaN or infinity
-                const bool boundary = MOD && (kbase < key_all0 || kbase + C::kTP > key_all1);
-                if (__any_sync(0xffffffffu, stale) || boundary) {
+                const bool stale = kbase + r >= key_end || pgi >= np || ((bad >> pgi) & 1);
+                if (__any_sync(0xffffffffu, stale)) {
                     // the entry's previous fill (stage j - kVSlots) must have been consumed first: its P.V done
                     // means that fill landed, so the wait below cannot pass on that older phase's parity
                     const int jp = j - C::kVSlots;
@@ -545,18 +472,6 @@ __global__ void __launch_bounds__(384, 1)
                         const uint32_t vrow = ring + ev * C::kEntry + half * C::kBoxB + r * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) sts128_zero(vrow + c * 16);
-                    } else if (MOD && boundary) {
-                        const uint32_t vrow = ring + ev * C::kEntry + half * C::kBoxB + r * 128;
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 v = lds128(vrow + c * 16);
-                            if (has_nonfinite16<kBF16>(v)) {
-                                *reinterpret_cast<volatile int*>(smem + C::kOffDirty) = 1;
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(vrow + c * 16),
-                                             "r"(v.x ^ nonfinite16<kBF16>(v.x)), "r"(v.y ^ nonfinite16<kBF16>(v.y)),
-                                             "r"(v.z ^ nonfinite16<kBF16>(v.z)), "r"(v.w ^ nonfinite16<kBF16>(v.w))
-                                             : "memory");
-                            }
-                        }
                     }
                 }
             }
@@ -569,50 +484,13 @@ __global__ void __launch_bounds__(384, 1)
         bool okl = ok;
         if (wait(okl, o_full, 0)) tc_fence_after();
         const float l_all = l + meet(l, okl);
-        bool dirty = false;
-        if constexpr (MOD) {
-            named_bar_sync(5, 32 * C::kSoftmaxWarps);  // every softmax warp is done with its stages
-            dirty = *reinterpret_cast<volatile int*>(smem + C::kOffDirty) != 0;
-        }
         if (okl) {
             float* dst = p.out + qrow * DH + half * kH;
-            const float inv = (MOD ? l_all != 0.f : l_all > 0.f) ? 1.f / l_all : 0.f;
+            const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
             uint32_t a[32], b2[32];
             tmem_ld32(tO + lane_addr + half * kH, a);
             tmem_ld32(tO + lane_addr + half * kH + 32, b2);
             tmem_wait_ld();
-            if constexpr (MOD) {
-                if (n_st > kFlush && row_valid) {  // the sums of the earlier accumulations
-                    const float4* sums = reinterpret_cast<const float4*>(dst);
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 v = sums[i / 4];
-                        uint32_t* x = i < 32 ? a + i : b2 + i - 32;
-                        x[0] = __float_as_uint(fmaf(v.x, sum_scale, __uint_as_float(x[0])));
-                        x[1] = __float_as_uint(fmaf(v.y, sum_scale, __uint_as_float(x[1])));
-                        x[2] = __float_as_uint(fmaf(v.z, sum_scale, __uint_as_float(x[2])));
-                        x[3] = __float_as_uint(fmaf(v.w, sum_scale, __uint_as_float(x[3])));
-                    }
-                }
-                // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for
-                // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
-                // values, read again, say what those sums are.
-                bool again = dirty;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float x = __uint_as_float(a[i]), y = __uint_as_float(b2[i]);
-                    again = again || x != x || y != y;
-                }
-                if (again && row_valid && l_all == l_all) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        uint32_t& x = i < 32 ? a[i & 31] : b2[i & 31];
-                        const float s = sum_nonfinite<kBF16>(p, b, kvh, P, DH, half * kH + i, row_lo, row_hi);
-                        const float o = __uint_as_float(x);
-                        x = __float_as_uint(o != o ? s : o + s);
-                    }
-                }
-            }
             if (row_valid) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
@@ -633,33 +511,6 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
-}
-
-// Compiled instances are in prefill_tc.cu and prefill_tc_mod.cu.
-template <int KT, int P, bool MOD = false>
-cudaError_t launch_prefill_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
-                                   cudaStream_t st) {
-    using C = PfCfg<128, P>;
-    auto* kern = paged_prefill_tc_kernel<KT, 128, P, MOD>;
-    static std::atomic<uint64_t> configured{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(configured.load(std::memory_order_acquire) & bit)) {
-        // the kernel moves registers between its warpgroups (setmaxnreg): the shares must fit in what a CTA
-        // is launched with, or the warpgroup asking for more would wait for ever
-        cudaFuncAttributes fa{};
-        e = cudaFuncGetAttributes(&fa, kern);
-        if (e != cudaSuccess) return e;
-        const long long pool = static_cast<long long>(fa.numRegs) * C::kThreads;
-        const long long need = 128LL * C::kRegsLow + 256LL * C::kRegsHigh;
-        if (need > pool) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-        configured.fetch_or(bit, std::memory_order_acq_rel);
-    }
-    return launch_pdl(kern, grid, dim3(C::kThreads), C::kSmem, st, p, tk, tv);
 }
 
 }  // namespace kvp

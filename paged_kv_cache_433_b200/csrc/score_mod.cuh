@@ -63,46 +63,75 @@ __device__ __forceinline__ float tanh_any(float u) {
 // x = q . k, the capped score in log2 units is x times a polynomial in x^2 whose coefficients the host scales by
 // the powers of (scale / c)^2 (p.cap_coef), valid for |x| <= p.cap_small.
 constexpr int kCapTerms = 6;
+// max(|a|, |b|, |c|) in one instruction (three-input form, sm_100)
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 constexpr double kTanhSmall = 0.75;
 constexpr double kTanhPoly[kCapTerms] = {0.999999971, -0.333329589, 0.13325406, -0.0533444284, 0.0195829047, -0.00471625478};
-__device__ __forceinline__ float2 cap_small2(const DecodeParams& p, float2 x) {
-    const float2 z = fmul2(x, x);
-    float2 r = make_float2(p.cap_coef[5], p.cap_coef[5]);
+// And for |u| <= kTanhTiny degree 2 (1.1e-7): three operations fewer a pair, which the chunked prefill feels.
+constexpr int kCapTinyTerms = 3;
+constexpr double kTanhTiny = 0.2;
+constexpr double kTanhTinyPoly[kCapTinyTerms] = {0.999999895, -0.333285909, 0.130154075};
+// Chunked prefill: the largest cap (log2 units) with one softmax reference for all rows.
+constexpr float kFixedRefMax = 80.f;
+// The coefficients as packed pairs in registers: loaded once through volatile moves, or the compiler fetches both
+// halves of each again for every pair of scores (the packed operations take no constant-bank operand).
+struct CapCoef {
+    float2 c[kCapTerms];
+};
+__device__ __forceinline__ CapCoef cap_coefs(const DecodeParams& p) {
+    CapCoef k;
 #pragma unroll
-    for (int i = kCapTerms - 2; i >= 0; --i) r = ffma2(z, r, make_float2(p.cap_coef[i], p.cap_coef[i]));
+    for (int i = 0; i < kCapTerms; ++i)
+        asm volatile("{\n\tmov.b32 %0, %2;\n\tmov.b32 %1, %2;\n\t}" : "=f"(k.c[i].x), "=f"(k.c[i].y) : "f"(p.cap_coef[i]));
+    return k;
+}
+__device__ __forceinline__ float2 cap_small2(const CapCoef& k, float2 x) {
+    const float2 z = fmul2(x, x);
+    float2 r = k.c[kCapTerms - 1];
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) r = ffma2(z, r, k.c[i]);
     return fmul2(x, r);
 }
 
 // x[0 .. 1] of every pair: products -> capped (or only scaled) scores in log2 units. Called by whole warps.
 template <int N>
-__device__ __forceinline__ void cap_scores(const DecodeParams& p, float (&x)[N]) {
+__device__ __forceinline__ void cap_scores(const DecodeParams& p, const CapCoef& k, float (&x)[N]) {
     if (p.cap_out != 0.f) {
-        float big = 0.f;
+        float big = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-        for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(x[c]));
+        for (int c = 2; c < N; c += 2) big = fmax3_abs(big, x[c], x[c + 1]);
         if (__any_sync(0xffffffffu, big > p.cap_small)) {
 #pragma unroll
             for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c] * p.cap_in) * p.cap_out;
         } else {
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
-                const float2 t = cap_small2(p, make_float2(x[c], x[c + 1]));
+                const float2 t = cap_small2(k, make_float2(x[c], x[c + 1]));
                 x[c] = t.x;
                 x[c + 1] = t.y;
             }
         }
     } else {
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-        for (int c = 0; c < N; ++c) x[c] *= p.scale_log2;
+        for (int c = 0; c < N; c += 2) {
+            const float2 t = fmul2(make_float2(x[c], x[c + 1]), sl2);
+            x[c] = t.x;
+            x[c + 1] = t.y;
+        }
     }
 }
 
 // Products of one warp's MMA tiles, query rows as MMA rows: sc[n][e] is row e / 2, token n * 8 + (e & 1) of the stage
 // counted from the lane's first; dist0 / dist1: position minus that first token for rows 0 / 1.
 template <int NT>
-__device__ __forceinline__ void modify_rows(const DecodeParams& p, float (&sc)[NT][4], const float (&slope)[2], int dist0,
-                                            int dist1) {
-    cap_scores(p, reinterpret_cast<float(&)[NT * 4]>(sc));
+__device__ __forceinline__ void modify_rows(const DecodeParams& p, const CapCoef& k, float (&sc)[NT][4],
+                                            const float (&slope)[2], int dist0, int dist1) {
+    cap_scores(p, k, reinterpret_cast<float(&)[NT * 4]>(sc));
     if (p.alibi_slopes != nullptr) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -115,9 +144,9 @@ __device__ __forceinline__ void modify_rows(const DecodeParams& p, float (&sc)[N
 // The same with heads as MMA columns: sc[nt][mt][e] is head column e & 1 of tile nt, token mt * 16 + 8 (e / 2) counted
 // from the lane's first; dist: the query's position minus that first token.
 template <int NT, int MT>
-__device__ __forceinline__ void modify_cols(const DecodeParams& p, float (&sc)[NT][MT][4], const float (&slope)[NT][2],
-                                            int dist) {
-    cap_scores(p, reinterpret_cast<float(&)[NT * MT * 4]>(sc));
+__device__ __forceinline__ void modify_cols(const DecodeParams& p, const CapCoef& k, float (&sc)[NT][MT][4],
+                                            const float (&slope)[NT][2], int dist) {
+    cap_scores(p, k, reinterpret_cast<float(&)[NT * MT * 4]>(sc));
     if (p.alibi_slopes != nullptr) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -130,10 +159,67 @@ __device__ __forceinline__ void modify_cols(const DecodeParams& p, float (&sc)[N
     }
 }
 
-// The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key.
-template <int N>
-__device__ __forceinline__ void modify_row(const DecodeParams& p, float (&s)[N], float slope, int dist0) {
-    cap_scores(p, s);
+// The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key. FIXED: minus
+// p.fixed_ref (a cap is set and no bias).
+struct CapRowCoef {
+    CapCoef small;
+    float2 tiny[kCapTinyTerms], neg_ref;
+};
+__device__ __forceinline__ CapRowCoef cap_row_coefs(const DecodeParams& p) {
+    CapRowCoef k;
+    k.small = cap_coefs(p);
+    auto pair = [](float x) {
+        float2 v;
+        asm volatile("{\n\tmov.b32 %0, %2;\n\tmov.b32 %1, %2;\n\t}" : "=f"(v.x), "=f"(v.y) : "f"(x));
+        return v;
+    };
+#pragma unroll
+    for (int i = 0; i < kCapTinyTerms; ++i) k.tiny[i] = pair(p.cap_coef_tiny[i]);
+    k.neg_ref = pair(-p.fixed_ref);
+    return k;
+}
+template <bool FIXED, int N>
+__device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCoef& k, float (&s)[N], float slope,
+                                           int dist0) {
+    if (FIXED || p.cap_out != 0.f) {
+        float big = fmaxf(fabsf(s[0]), fabsf(s[1]));
+#pragma unroll
+        for (int c = 2; c < N; c += 2) big = fmax3_abs(big, s[c], s[c + 1]);
+        auto last = [&](float2 x, float2 r) { return FIXED ? ffma2(x, r, k.neg_ref) : fmul2(x, r); };
+        if (!__any_sync(0xffffffffu, big > p.cap_tiny)) {
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+                const float2 x = make_float2(s[c], s[c + 1]), z = fmul2(x, x);
+                const float2 t = last(x, ffma2(z, ffma2(z, k.tiny[2], k.tiny[1]), k.tiny[0]));
+                s[c] = t.x;
+                s[c + 1] = t.y;
+            }
+        } else if (!__any_sync(0xffffffffu, big > p.cap_small)) {
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+                const float2 x = make_float2(s[c], s[c + 1]), z = fmul2(x, x);
+                float2 r = k.small.c[kCapTerms - 1];
+#pragma unroll
+                for (int i = kCapTerms - 2; i >= 0; --i) r = ffma2(z, r, k.small.c[i]);
+                const float2 t = last(x, r);
+                s[c] = t.x;
+                s[c + 1] = t.y;
+            }
+        } else {
+            const float ref = FIXED ? p.fixed_ref : 0.f;
+#pragma unroll
+            for (int c = 0; c < N; ++c) s[c] = tanh_any(s[c] * p.cap_in) * p.cap_out - ref;
+        }
+    } else {
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const float2 t = fmul2(make_float2(s[c], s[c + 1]), sl2);
+            s[c] = t.x;
+            s[c + 1] = t.y;
+        }
+    }
+    if (FIXED) return;
     if (p.alibi_slopes != nullptr) {
         const float d = static_cast<float>(dist0);
 #pragma unroll
