@@ -17,6 +17,8 @@
 //   - FIXED (bf16, a cap of at most 55, no bias): the cap bounds the scores, one
 //     reference serves every row, and neither maximum nor barrier is needed; the
 //     reference is subtracted by the last multiply-add of the cap's polynomial.
+//     Three softmax warpgroups then work on different stages, one row per
+//     thread in chunks of 32 keys, so that one computes while the others wait.
 //   - hi is rounded, not truncated (pack2_split_near), and O is moved into fp32
 //     sums in registers every kFlushKeys keys: against 64 bits the error is 7e-6
 //     of the result at any length (1.1e-5 at 4096 keys, 7.5e-5 at 32K without).
@@ -41,7 +43,7 @@
 
 namespace kvp {
 
-template <int DH, int P>
+template <int DH, int P, bool FIXED>
 struct PfModCfg {
     static constexpr int kTP = 128;              // keys per stage
     static constexpr int kPPS = kTP / P;         // pages per stage
@@ -54,11 +56,13 @@ struct PfModCfg {
     static constexpr int kRing = kKSlots + kVSlots;
     static constexpr int kQB = 128 * DH * 2;     // Q tile: 128 rows
     static constexpr int kOffQ = kRing * kEntry;
-    static constexpr int kParts = 2;             // threads per row, each with half of a stage's keys and of the dims
+    // threads per row: each with half of a stage's keys and of the dims; FIXED: each with every third stage and up to
+    // 48 of the dims
+    static constexpr int kParts = FIXED ? 3 : 2;
     static constexpr int kOffX = kOffQ + kQB;    // row exchange: [2][kParts][128] floats + ints
     static constexpr int kOffBar = kOffX + 2 * kParts * 128 * 4 * 2;
-    // full[R], empty[R], q_full, s_full[3], p_full[3], p_empty[3], o_full, done (QK), done (PV)
-    static constexpr int kNumBars = 2 * kRing + 1 + 3 + 3 + 3 + 3;
+    // full[R], empty[R], q_full, s_full[3], p_full[3], p_empty[3], o_full, done (QK), done (PV), o_free
+    static constexpr int kNumBars = 2 * kRing + 1 + 3 + 3 + 3 + 4;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffDirty = kOffTmem + 8;  // a boundary stage held a NaN or an infinity in V
     static constexpr int kSmem = 1024 + kOffTmem + 16;
@@ -66,9 +70,9 @@ struct PfModCfg {
     static constexpr int kVWarp = 2;             // the V producer (warp 0 produces K)
     static constexpr int kPVWarp = 3;            // issues P.V (warp 1 issues QK)
     static constexpr int kFirstSoftmaxWarp = 4;
-    // registers per thread after the split: warpgroup 0 (producers, issuers) and the softmax warpgroups;
+    // registers per thread after the split: warpgroup 0 (producers, issuers) and the two softmax warpgroups;
     // 128 x kRegsLow + 256 x kRegsHigh must not exceed the launch's 384 x (registers per thread), which the
-    // host checks before the first launch
+    // host checks before the first launch. FIXED: 512 threads of 128 registers, no split.
     static constexpr uint32_t kRegsLow = 64, kRegsHigh = 216;
     static constexpr int kSoftmaxWarps = 4 * kParts;
     static constexpr uint32_t kTmemCols = 512;   // S x 3 (384) + O (128)
@@ -77,11 +81,16 @@ struct PfModCfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
+// Bits 0 .. n - 1 of 64 (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ uint64_t bits_below(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 template <int KT, int DH, int P, bool FIXED>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
     paged_prefill_mod_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v) {
-    using C = PfModCfg<DH, P>;
+    using C = PfModCfg<DH, P, FIXED>;
     constexpr bool kBF16 = KT == KV_DTYPE_BF16;
     constexpr int kParts = C::kParts;
     constexpr uint32_t kIdescQK = idesc_f16(kBF16, 128, C::kTP, false, false);
@@ -156,6 +165,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t o_full = q_full + 80;
     const uint32_t done_qk = q_full + 88;
     const uint32_t done_pv = q_full + 96;
+    const uint32_t o_free = q_full + 104;  // FIXED: every softmax warp has moved O into its sums
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffTmem);
 
     if (threadIdx.x == 0) {
@@ -165,7 +175,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         mbar_init(q_full, C::kSoftmaxWarps);
         for (int i = 0; i < 3; ++i) mbar_init(s_full(i), 1);
-        for (int i = 0; i < 3; ++i) mbar_init(p_full(i), C::kSoftmaxWarps);
+        for (int i = 0; i < 3; ++i) mbar_init(p_full(i), FIXED ? 4 : C::kSoftmaxWarps);
+        mbar_init(o_free, C::kSoftmaxWarps);
         for (int i = 0; i < 3; ++i) mbar_init(p_empty(i), 1);
         mbar_init(o_full, 1);
         mbar_init(done_qk, 1);
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(384, 1)
     // the register split sits at the top of each warpgroup's branch, so every code path after it is
     // compiled for its own budget
     if (warp < C::kFirstSoftmaxWarp) {
-    regs_dec<C::kRegsLow>();
+    if constexpr (!FIXED) regs_dec<C::kRegsLow>();
     if (warp == 0 || warp == C::kVWarp) {
         // ------------------------------------------------------------ producers
         // warp 0 issues the K boxes of every stage, warp kVWarp the V boxes: two streams of TMA requests
@@ -284,18 +295,21 @@ __global__ void __launch_bounds__(384, 1)
                     const int e = vslot(j);
                     if (!wait(full(e), vphase(j))) break;
                     if (!wait(p_full(j % 3), (j / 3) & 1)) break;
+                    if (FIXED && j > 0 && j % kFlush == 0 && !wait(o_free, (j / kFlush - 1) & 1)) break;
                     tc_fence_after();
                     const uint32_t sV = ring + e * C::kEntry;
                     const uint32_t tP = tmem + (j % 3) * C::kTP;
-                    // each half of the keys: 32 columns of values, then 32 of residuals, over its own S columns
-                    auto p_col = [](int kk) { return (kk >> 2) * (C::kTP / 2) + (kk & 3) * 8; };
+                    // each run of 64 keys (FIXED: 32), as one thread writes it over its own S columns: the values, then
+                    // their residuals
+                    constexpr int kRun = FIXED ? 32 : 64;
+                    auto p_col = [](int kk) { return kk * 16 / kRun * kRun + kk * 16 % kRun / 2; };
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
                         umma_ts(tO, tP + p_col(kk), smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128), kIdescPV,
                                 (j % kFlush != 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
-                        umma_ts(tO, tP + p_col(kk) + C::kTP / 4, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128),
+                        umma_ts(tO, tP + p_col(kk) + kRun / 2, smem_desc(sV + kk * 16 * 128, C::kBoxB, 1024, kSwz128),
                                 kIdescPV, 1u);
                     umma_commit(empty(e));
                     umma_commit(p_empty(j % 3));
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
     }
     } else {
-        regs_inc<C::kRegsHigh>();
+        if constexpr (!FIXED) regs_inc<C::kRegsHigh>();
         // ------------------------------------------------------------ Q tile, softmax, epilogue
         const int quarter = warp & 3;
         const int part = (warp - C::kFirstSoftmaxWarp) >> 2;  // key columns [kH part, + kH) of S, dims of O likewise
@@ -331,17 +345,13 @@ __global__ void __launch_bounds__(384, 1)
         float* xm = reinterpret_cast<float*>(smem + C::kOffX);  // [buf][part][row] maxima / sums
         int* xok = reinterpret_cast<int*>(smem + C::kOffX) + 2 * kParts * 128;
         int xbuf = 0;
-        // this thread's 64 bytes of Q row r (and of V row r where that has to be looked at): box column part / 2,
-        // 16-byte chunks 4 (part % 2) .. + 3
-        constexpr int kRowChunks = 16 / kParts;
-        const int box = part * kRowChunks / 8, chunk0 = part * kRowChunks % 8;
+        // Q row r -> the swizzled K-major tile, its sixteen 16-byte chunks shared out over the parts
         {
-            const uint4* src = static_cast<const uint4*>(p.q) + qrow * (DH / 8) + part * kRowChunks;
-#pragma unroll
-            for (int c = 0; c < kRowChunks; ++c) {
+            const uint4* src = static_cast<const uint4*>(p.q) + qrow * (DH / 8);
+            for (int c = part; c < DH / 8; c += kParts) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (row_valid) v = src[c];
-                const uint32_t dst = sQ + box * (128 * 128) + r * 128 + (((chunk0 + c) ^ (r & 7)) << 4);
+                const uint32_t dst = sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
                              "r"(v.w)
                              : "memory");
@@ -376,7 +386,8 @@ __global__ void __launch_bounds__(384, 1)
         };
         const CapRowCoef coef = cap_row_coefs(p);
         float m_ref = FIXED ? p.fixed_ref : -INFINITY, l = 0.f;
-        constexpr int kH = C::kTP / kParts;  // key columns per thread
+        constexpr int kH = FIXED ? 48 : C::kTP / kParts;  // dims of O per thread (and, not FIXED, keys per stage)
+        const int od = part * kH;                          // first of them
         // earlier accumulations of this thread's part of O, in units of the current reference
         float2 acc[kH / 2];
 #pragma unroll
@@ -384,8 +395,38 @@ __global__ void __launch_bounds__(384, 1)
         // lanes 0 .. kPPS-1: the page ids of stage j, read one stage ahead; the mask of pages the producers
         // skip (entries outside the pool) is then known without waiting for the V entry
         const int32_t* trow = p.block_tables + (int64_t)b * p.max_blocks + page_first;
-        int pg_cur = lane < C::kPPS && lane < n_pages ? __ldg(trow + lane) : -1;
-        for (int j = 0; j < n_st; ++j) {
+        int pg_cur = !FIXED && lane < C::kPPS && lane < n_pages ? __ldg(trow + lane) : -1;
+        // A key no row may see (past the tile, or on a page not loaded) may hold stale bytes: zero its V row (this thread:
+        // `n` 16-byte chunks of V row r from `chunk` on) once the V entry has landed. In a stage that some rows see only in
+        // part a NaN or an infinity in V must not reach the others as 0 times it: those elements are zeroed too, and
+        // noted. Only warps with such a row wait for the entry (the P.V issuer waits for every entry).
+        auto clean_v = [&](int j, int kbase, int np, int bad, int chunk, int n, bool& okl) {
+            const int pgi = r / P;
+            const bool stale = kbase + r >= key_end || kbase + r < key_begin || pgi >= np || ((bad >> pgi) & 1);
+            const bool boundary = kbase < key_all0 || kbase + C::kTP > key_all1;
+            if (!__any_sync(0xffffffffu, stale) && !boundary) return;
+            // the entry's previous fill (stage j - kVSlots) must have been consumed first: its P.V done means that
+            // fill landed, so the wait below cannot pass on that older phase's parity
+            const int ev = vslot(j), jp = j - C::kVSlots;
+            if (jp >= 0 && !wait(okl, p_empty(jp % 3), (jp / 3) & 1)) return;
+            if (!wait(okl, full(ev), vphase(j))) return;
+            for (int c = chunk; c < chunk + n; ++c) {
+                const uint32_t at = ring + ev * C::kEntry + (c >> 3) * C::kBoxB + r * 128 + (c & 7) * 16;
+                if (stale) {
+                    sts128_zero(at);
+                } else if (boundary) {
+                    const uint4 v = lds128(at);
+                    if (has_nonfinite16<kBF16>(v)) {
+                        *reinterpret_cast<volatile int*>(smem + C::kOffDirty) = 1;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x ^ nonfinite16<kBF16>(v.x)),
+                                     "r"(v.y ^ nonfinite16<kBF16>(v.y)), "r"(v.z ^ nonfinite16<kBF16>(v.z)),
+                                     "r"(v.w ^ nonfinite16<kBF16>(v.w))
+                                     : "memory");
+                    }
+                }
+            }
+        };
+        for (int j = 0; !FIXED && j < n_st; ++j) {
             bool okl = ok;
             const uint32_t tS = tmem + (j % 3) * C::kTP + lane_addr;
             const int nxt = (j + 1) * C::kPPS + lane;
@@ -401,7 +442,6 @@ __global__ void __launch_bounds__(384, 1)
                 for (int i = 0; i < kH; ++i) s[i] = __uint_as_float(a[i / 32][i % 32]);
             }
             // keys of this stage: kbase .. kbase + 127
-            const int ev = vslot(j);
             const int kbase = key_first + j * C::kTP;
             const int np = min(C::kPPS, n_pages - j * C::kPPS);
             const unsigned loaded = __ballot_sync(0xffffffffu, lane < np && pg_cur >= 0 && pg_cur < p.num_pages);
@@ -410,22 +450,24 @@ __global__ void __launch_bounds__(384, 1)
             // this row sees keys [low, lim) of the stage; pages skipped or not loaded are masked
             const int lim = row_valid ? min(C::kTP, row_hi - kbase) : 0;
             const int low = row_lo - kbase;
-            modify_row<FIXED>(p, coef, s, slope, pos - kbase - part * kH);
+            modify_row<false>(p, coef, s, slope, pos - kbase - part * kH);
             if (!(lim == C::kTP && np == C::kPPS && bad == 0 && low <= 0 && okl)) {
+                // this thread's visible columns as bits: from low to lim, on loaded pages
+                constexpr int kPer = kH / P;  // pages among this thread's columns
+                const int c0 = part * kH;
+                uint64_t see = bits_below(lim - c0) & ~bits_below(low - c0);
 #pragma unroll
-                for (int c = 0; c < kH; ++c) {
-                    const int cc = part * kH + c, pgi = cc / P;
-                    if (!okl || cc >= lim || cc < low || pgi >= np || ((bad >> pgi) & 1)) s[c] = -INFINITY;
-                }
+                for (int k = 0; k < kPer; ++k)
+                    if (part * kPer + k >= np || ((bad >> (part * kPer + k)) & 1))
+                        see &= ~(((1ull << P) - 1) << (k * P));
+                if (!okl) see = 0;
+#pragma unroll
+                for (int c = 0; c < kH; ++c)
+                    if (!((static_cast<uint32_t>(see >> (c & 32)) >> (c & 31)) & 1u)) s[c] = -INFINITY;
             }
             float alpha = 1.f;
             bool need = false;
-            if constexpr (FIXED) {
-                if (!okl) {
-                    ok = false;
-                    break;
-                }
-            } else {
+            {
                 // reference maximum: moves only when the row's max exceeds it by more than 2^8. The two warps of a row
                 // meet in one barrier that votes whether any of its rows may have to; only then are the maxima exchanged.
                 float mx = fmaxf(s[0], s[1]);
@@ -474,7 +516,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 tmem_wait_st();
             }
-            if (!FIXED && __any_sync(0xffffffffu, need)) {
+            if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
                 for (int i = 0; i < kH / 2; ++i) acc[i] = fmul2(acc[i], make_float2(alpha, alpha));
             }
@@ -487,9 +529,8 @@ __global__ void __launch_bounds__(384, 1)
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    // two keys at a time: one packed add for the exponents (FIXED: done with the cap), one for the sums
-                    float2 x = make_float2(s[q * 32 + 2 * i], s[q * 32 + 2 * i + 1]);
-                    if constexpr (!FIXED) x = fadd2(x, negv);
+                    // two keys at a time: one packed add for the exponents, one for the sums
+                    const float2 x = fadd2(make_float2(s[q * 32 + 2 * i], s[q * 32 + 2 * i + 1]), negv);
                     const float p0 = exp2f(x.x), p1 = exp2f(x.y);  // exp2(-inf) = 0 for masked keys
                     lsum = fadd2(lsum, make_float2(p0, p1));
                     pack2_split_near<kBF16>(p0, p1, hi[i], lo[i]);
@@ -499,50 +540,99 @@ __global__ void __launch_bounds__(384, 1)
             }
             l += lsum.x + lsum.y;
             tmem_wait_st();
-            // a key no row may see (past the tile, or on a page not loaded) may hold stale bytes: zero its V row (this
-            // thread: 64 bytes of V row r) once the V entry has landed. In a stage that some rows see only in part a
-            // NaN or an infinity in V must not reach the others as 0 times it: those elements are zeroed too, and
-            // noted. Only warps with such a row wait for the entry (the P.V issuer waits for every entry).
-            {
-                const int pgi = r / P;
-                const bool stale = kbase + r >= key_end || kbase + r < key_begin || pgi >= np || ((bad >> pgi) & 1);
-                const bool boundary = kbase < key_all0 || kbase + C::kTP > key_all1;
-                if (__any_sync(0xffffffffu, stale) || boundary) {
-                    // the entry's previous fill (stage j - kVSlots) must have been consumed first: its P.V done
-                    // means that fill landed, so the wait below cannot pass on that older phase's parity
-                    const int jp = j - C::kVSlots;
-                    if (jp >= 0 && !wait(okl, p_empty(jp % 3), (jp / 3) & 1)) {
-                        ok = false;  // the next vote stops the quarter
-                        continue;
-                    }
-                    if (!wait(okl, full(ev), vphase(j))) {
-                        ok = false;  // the next vote stops the quarter
-                        continue;
-                    }
-                    const uint32_t vrow = ring + ev * C::kEntry + box * C::kBoxB + r * 128 + chunk0 * 16;
-                    if (stale) {
-#pragma unroll
-                        for (int c = 0; c < kRowChunks; ++c) sts128_zero(vrow + c * 16);
-                    } else if (boundary) {
-#pragma unroll
-                        for (int c = 0; c < kRowChunks; ++c) {
-                            const uint4 v = lds128(vrow + c * 16);
-                            if (has_nonfinite16<kBF16>(v)) {
-                                *reinterpret_cast<volatile int*>(smem + C::kOffDirty) = 1;
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(vrow + c * 16),
-                                             "r"(v.x ^ nonfinite16<kBF16>(v.x)), "r"(v.y ^ nonfinite16<kBF16>(v.y)),
-                                             "r"(v.z ^ nonfinite16<kBF16>(v.z)), "r"(v.w ^ nonfinite16<kBF16>(v.w))
-                                             : "memory");
-                            }
-                        }
-                    }
-                }
+            clean_v(j, kbase, np, bad, part * 8, 8, okl);
+            if (!okl) {
+                ok = false;  // the next vote stops the quarter
+                continue;
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full(j % 3));
         }
+        // FIXED: the three softmax warpgroups take every third stage, each its own S buffer, a thread a whole row of 128
+        // keys in four chunks. Nothing passes between them but O: while one waits for its scores the others compute.
+        int next_flush = kFlush;
+        // before stage next_flush, whose P.V starts a new accumulation: this thread's part of O joins its sums
+        auto move_o = [&](bool& okl) {
+            const int jf = next_flush, jp = jf - 1;
+            next_flush += kFlush;
+            // S(jf) is there: P.V(jf - 3) is done, hence P.V(jp - 3), so that the second wait's parity is that of P.V(jp)
+            if (!wait(okl, s_full(jf % 3), (jf / 3) & 1) || !wait(okl, p_empty(jp % 3), (jp / 3) & 1)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < kH / 16; ++q) {
+                if (od + q * 16 >= DH) break;
+                uint32_t a[16];
+                tmem_ld16(tO + lane_addr + od + q * 16, a);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[q * 8 + i] = fadd2(acc[q * 8 + i], make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+        };
+        for (int j = part; FIXED && j < n_st && ok; j += kParts) {
+            if (!wait(ok, s_full(j % 3), (j / 3) & 1)) break;
+            while (next_flush <= j && ok) move_o(ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tmem + (j % 3) * C::kTP + lane_addr;
+            const int kbase = key_first + j * C::kTP;
+            const int np = min(C::kPPS, n_pages - j * C::kPPS);
+            const int pg = lane < np ? __ldg(trow + j * C::kPPS + lane) : -1;
+            const unsigned loaded = __ballot_sync(0xffffffffu, lane < np && pg >= 0 && pg < p.num_pages);
+            const int bad = static_cast<int>(~loaded & ((1u << np) - 1u));
+            const int lim = row_valid ? row_hi - kbase : 0, low = row_lo - kbase;
+            const bool full_stage = lim >= C::kTP && np == C::kPPS && bad == 0 && low <= 0;
+            float2 lsum = make_float2(0.f, 0.f);
+            // (one copy of the chunk's code: unrolled four times it outgrows the instruction caches)
+#pragma unroll 1
+            for (int q = 0; q < C::kTP / 32; ++q) {
+                uint32_t a[32];
+                tmem_ld32(tS + q * 32, a);
+                tmem_wait_ld();
+                float s[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(a[i]);
+                modify_row<true>(p, coef, s, 0.f, 0);
+                if (!full_stage) {
+                    uint32_t see = static_cast<uint32_t>(bits_below(lim - q * 32) & ~bits_below(low - q * 32));
+#pragma unroll
+                    for (int k = 0; k < 32 / P; ++k) {
+                        const int pgi = q * (32 / P) + k;
+                        if (pgi >= np || ((bad >> pgi) & 1)) see &= P == 32 ? 0u : ~(0xffffu << (k * 16));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((see >> c) & 1u)) s[c] = -INFINITY;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 = exp2f(s[h * 16 + 2 * i]), p1 = exp2f(s[h * 16 + 2 * i + 1]);
+                        lsum = fadd2(lsum, make_float2(p0, p1));
+                        pack2_split_near<kBF16>(p0, p1, hi[i], lo[i]);
+                    }
+                    tmem_st8(tS + q * 32 + h * 8, hi);
+                    tmem_st8(tS + q * 32 + 16 + h * 8, lo);
+                }
+            }
+            l += lsum.x + lsum.y;
+            tmem_wait_st();
+            clean_v(j, kbase, np, bad, 0, 16, ok);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(j % 3));
+        }
+        while (FIXED && ok && next_flush < n_st) move_o(ok);
+
         // ---- epilogue: O row / l (this thread: dims kH part .. + kH - 1)
         bool okl = ok;
         if (wait(okl, o_full, 0)) tc_fence_after();
@@ -553,40 +643,44 @@ __global__ void __launch_bounds__(384, 1)
         for (int k = 0; k < kParts; ++k) l_all += lv[k];
         named_bar_sync(5, 32 * C::kSoftmaxWarps);  // every softmax warp is done with its stages
         const bool dirty = *reinterpret_cast<volatile int*>(smem + C::kOffDirty) != 0;
-        float* dst = p.out + qrow * DH + part * kH;
+        float* dst = p.out + qrow * DH + od;
         if (okl) {
             const float inv = l_all != 0.f ? 1.f / l_all : 0.f;
-            uint32_t a[kH / 32][32];
 #pragma unroll
-            for (int q = 0; q < kH / 32; ++q) tmem_ld32(tO + lane_addr + part * kH + q * 32, a[q]);
-            tmem_wait_ld();
-            if (row_valid) {
-                float o[kH];
+            for (int q = 0; q < kH / 16; ++q) {
+                if (od + q * 16 >= DH) break;
+                uint32_t a[16];
+                tmem_ld16(tO + lane_addr + od + q * 16, a);
+                tmem_wait_ld();
+                if (row_valid) {
+                    float o[16];
 #pragma unroll
-                for (int i = 0; i < kH; i += 2) {
-                    o[i] = __uint_as_float(a[i / 32][i % 32]) + acc[i / 2].x;
-                    o[i + 1] = __uint_as_float(a[i / 32][i % 32 + 1]) + acc[i / 2].y;
-                }
-                // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for
-                // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
-                // values, read again, say what those sums are.
-                bool again = dirty;
-#pragma unroll
-                for (int i = 0; i < kH; ++i) again = again || o[i] != o[i];
-                if (again && l_all == l_all) {
-#pragma unroll
-                    for (int i = 0; i < kH; ++i) {
-                        const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, part * kH + i, row_lo, row_hi);
-                        o[i] = o[i] != o[i] ? x : o[i] + x;
+                    for (int i = 0; i < 16; i += 2) {
+                        o[i] = __uint_as_float(a[i]) + acc[q * 8 + i / 2].x;
+                        o[i + 1] = __uint_as_float(a[i + 1]) + acc[q * 8 + i / 2].y;
                     }
-                }
+                    // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for
+                    // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
+                    // values, read again, say what those sums are.
+                    bool again = dirty;
 #pragma unroll
-                for (int i = 0; i < kH; i += 4)
-                    *reinterpret_cast<float4*>(dst + i) =
-                        make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                    for (int i = 0; i < 16; ++i) again = again || o[i] != o[i];
+                    if (again && l_all == l_all) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi);
+                            o[i] = o[i] != o[i] ? x : o[i] + x;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(dst + q * 16 + i) =
+                            make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                }
+                __syncwarp();  // the next load is warp-collective
             }
         } else if (row_valid) {
-            for (int d = 0; d < kH; ++d) dst[d] = 0.f;
+            for (int d = 0; d < kH && od + d < DH; ++d) dst[d] = 0.f;
         }
     }
 
@@ -599,7 +693,7 @@ __global__ void __launch_bounds__(384, 1)
 template <int KT, int P, bool FIXED>
 cudaError_t launch_prefill_mod_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                                        cudaStream_t st) {
-    using C = PfModCfg<128, P>;
+    using C = PfModCfg<128, P, FIXED>;
     auto* kern = paged_prefill_mod_tc_kernel<KT, 128, P, FIXED>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
@@ -613,8 +707,8 @@ cudaError_t launch_prefill_mod_tc_inst(const DecodeParams& p, const CUtensorMap&
         e = cudaFuncGetAttributes(&fa, kern);
         if (e != cudaSuccess) return e;
         const long long pool = static_cast<long long>(fa.numRegs) * C::kThreads;
-        const long long need = 128LL * C::kRegsLow + 128LL * C::kParts * C::kRegsHigh;
-        if (need > pool) return cudaErrorInvalidConfiguration;
+        const long long need = 128LL * C::kRegsLow + 256LL * C::kRegsHigh;
+        if (!FIXED && need > pool) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);

@@ -162,12 +162,10 @@ __device__ __forceinline__ void modify_cols(const DecodeParams& p, const CapCoef
 // The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key. FIXED: minus
 // p.fixed_ref (a cap is set and no bias).
 struct CapRowCoef {
-    CapCoef small;
     float2 tiny[kCapTinyTerms], neg_ref;
 };
 __device__ __forceinline__ CapRowCoef cap_row_coefs(const DecodeParams& p) {
     CapRowCoef k;
-    k.small = cap_coefs(p);
     auto pair = [](float x) {
         float2 v;
         asm volatile("{\n\tmov.b32 %0, %2;\n\tmov.b32 %1, %2;\n\t}" : "=f"(v.x), "=f"(v.y) : "f"(x));
@@ -196,14 +194,12 @@ __device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCo
             }
         } else if (!__any_sync(0xffffffffu, big > p.cap_small)) {
 #pragma unroll
-            for (int c = 0; c < N; c += 2) {
-                const float2 x = make_float2(s[c], s[c + 1]), z = fmul2(x, x);
-                float2 r = k.small.c[kCapTerms - 1];
+            for (int c = 0; c < N; ++c) {  // (scalar: the coefficients come from the constant bank)
+                const float z = s[c] * s[c];
+                float r = p.cap_coef[kCapTerms - 1];
 #pragma unroll
-                for (int i = kCapTerms - 2; i >= 0; --i) r = ffma2(z, r, k.small.c[i]);
-                const float2 t = last(x, r);
-                s[c] = t.x;
-                s[c + 1] = t.y;
+                for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, p.cap_coef[i]);
+                s[c] = FIXED ? fmaf(s[c], r, k.neg_ref.x) : s[c] * r;
             }
         } else {
             const float ref = FIXED ? p.fixed_ref : 0.f;
