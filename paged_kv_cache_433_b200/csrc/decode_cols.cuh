@@ -52,7 +52,12 @@
 namespace kvp {
 
 constexpr int kColsMaxB = 1024;      // sequences of a balanced launch
-constexpr int kColsItemTokens = 64;  // a row's fixed cost in tokens (its queries, its merge)
+#ifndef KVP_CW
+#define KVP_CW 4
+#define KVP_CC 3
+#endif
+constexpr int kColsWarps1 = KVP_CW, kColsCtas1 = KVP_CC;  // groups of at most 8 heads: consumer warps per CTA, CTAs per SM
+constexpr int kColsItemTokens = 128; // a row's fixed cost in tokens (its queries, its merge)
 constexpr int kColsMinTokens = 128;  // at least one stage per consumer warp and CTA
 
 template <int KT, int DH, int P, int NT, bool DUP>
@@ -72,8 +77,8 @@ struct ColsCfg {
     static constexpr int kChunk = kTP * kRowB;                   // K (or V) of one stage
     static constexpr int kStage = 2 * kChunk;
     static constexpr int kScaleB = kI8 ? P * 8 : 0;              // scales of one (page, head): K's P, then V's
-    static constexpr int kNC = 4;                                // consumer warps
-    static constexpr int kCtas = NT == 1 ? 3 : 2;                // CTAs per SM
+    static constexpr int kNC = NT == 1 ? kColsWarps1 : 4;        // consumer warps
+    static constexpr int kCtas = NT == 1 ? kColsCtas1 : 2;       // CTAs per SM
     // a warp's (O, m, l) fragments on their way to the warp that merges: [registers][lanes]
     static constexpr int kRegs = NT * (DH / 16) * 4 + 4 * NT;
     static constexpr int kMergeWarp = kRegs * (DUP ? 16 : 32) * 4;
@@ -86,7 +91,7 @@ struct ColsCfg {
     static constexpr int kOffBars = kOffScales + kNS * kUPS * kScaleB;
     static constexpr int kOffPages = kOffBars + 16 * kNS;        // bit j of word s: unit j of stage s was loaded
     static constexpr int kOffPre = kOffPages + 4 * kNS;          // balanced launch: prefix of the rows' spans
-    static constexpr int kSmem = 1024 + kOffPre + 4 * (kColsMaxB + 1) + 4 * 8;
+    static constexpr int kSmem = 1024 + kOffPre + 4 * (kColsMaxB + 1) + 4 * 16;
     static constexpr int kThreads = 32 * (kNC + 1);
     static_assert(P % kU == 0 && (kBoxInner == 128 || kBoxInner == 64), "shape");
     static_assert(kNS >= kNC, "a stage per consumer warp");
@@ -161,7 +166,7 @@ struct ColsWalk {
 };
 
 template <int KT, int QT, int DH, int P, int NT, bool DUP, bool MOD>
-__global__ void __launch_bounds__(160, (ColsCfg<KT, DH, P, NT, DUP>::kCtas))
+__global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (ColsCfg<KT, DH, P, NT, DUP>::kCtas))
     paged_decode_cols_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                              const __grid_constant__ CUtensorMap tmap_v) {
     using C = ColsCfg<KT, DH, P, NT, DUP>;

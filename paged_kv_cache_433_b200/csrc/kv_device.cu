@@ -449,7 +449,7 @@ int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_bl
     if (num_splits == 0) {
         const int sms = sm_count();
         if (sms <= 0) return KV_ERR_CUDA;
-        slots = static_cast<int64_t>(sms) * (g <= 8 ? 3 : 2);
+        slots = static_cast<int64_t>(sms) * (g <= 8 ? kColsCtas1 : 2);
     }
     const bool one_wave = static_cast<int64_t>(B) * H_kv * chunks <= slots;
     if (num_splits == 0 && !direct && !one_wave && B <= kColsMaxB && line < (1LL << 31)) {
