@@ -171,7 +171,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                              const __grid_constant__ CUtensorMap tmap_v) {
     using C = ColsCfg<KT, DH, P, NT, DUP>;
     constexpr bool kI8 = C::kI8;
-    constexpr bool kQBF16 = !kI8 && KT == KV_DTYPE_BF16;  // QK operands: bf16, else f16 (int8 codes are exact in both)
+    constexpr bool kQBF16 = KT == KV_DTYPE_BF16;         // QK operands of 16-bit K/V: bf16, else f16
     constexpr bool kPBF16 = kI8 || KT == KV_DTYPE_BF16;   // PV operands (int8: bf16, whose range holds any V scale)
     constexpr int kTP = C::kTP, kKS = DH / 16, kMT = kTP / 16, kOM = DH / 16, kUPS = C::kUPS;
     static_assert(!DUP || NT == 1, "doubled columns");
@@ -375,51 +375,58 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
     const int b = pc.b, kvh = pc.kvh, len = pc.len;
     const int head0 = kvh * p.g + hs * NT * 8;
     const int tok0 = pc.page0 * P;  // first token of the piece
-    // Q^T as the B operand: column lane / 4 of column tile nt is head nt * 8 + lane / 4 (DUP: 4 heads twice). 16-bit
-    // K/V: k-step kk covers dims kk*16 .. +15; int8: the lane's K words hold dims quad*Dh/4 + 4*kk .. +3.
-    uint32_t qb[NT][kKS][2];
-    float q_pow[NT][2];  // int8, bf16 q: what a row was divided by, for the lane's score columns
+    // Q^T as the B operand: column lane / 4 of column tile nt is head nt * 8 + lane / 4 (DUP: 4 heads twice).
+    constexpr int kQR = kI8 ? DH / 32 * 2 * 3 : kKS * 2;  // registers of a column tile
+    uint32_t qb[NT][kQR];
+    float q_pow[NT][2];  // int8: what a row was scaled by, for the lane's score columns, times the softmax scale
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int n = nt * 8 + r0;
         const int h = DUP ? n & 3 : n;
         const uint32_t* q32 = static_cast<const uint32_t*>(p.q) + (((int64_t)b * p.H_q + head0 + h) * DH >> 1);
-        float pow = 1.f;
-#pragma unroll
-        for (int kk = 0; kk < kKS; ++kk)
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                const int d = kI8 ? quad * (DH / 4) + 4 * kk + 2 * ch : kk * 16 + ch * 8 + 2 * quad;
-                qb[nt][kk][ch] = h < heads ? q32[d >> 1] : 0u;
-            }
-        if constexpr (kI8 && QT == KV_DTYPE_BF16) {
-            // the products with codes run in f16: a bf16 row is divided by a power of two that brings its largest
-            // magnitude to 2^14 (exact but for elements 2^-28 below it and smaller, whose rounding is at most 2^-39
-            // of the largest) and its scores are multiplied back: the whole bf16 range works
+        if constexpr (kI8) {
+            // The products with codes are exact integers: a row is scaled by a power of two that brings its largest
+            // magnitude to [2^21, 2^22), rounded to an integer (2^-23 of the largest at most) and split into three signed
+            // bytes, one MMA operand each. The lane holds dims quad*Dh/4 + 8*kk .. +7 of k-step kk, as its K words do.
+            float x[DH / 4];
             uint32_t top = 0;
 #pragma unroll
-            for (int kk = 0; kk < kKS; ++kk)
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    const uint32_t v = qb[nt][kk][ch];
-                    top = max(top, max((v << 16) & 0x7fffffffu, v & 0x7fff0000u));
-                }
+            for (int i = 0; i < DH / 8; ++i) {
+                const float2 v = unpack16<QT == KV_DTYPE_BF16>(h < heads ? q32[(quad * (DH / 4) >> 1) + i] : 0u);
+                x[2 * i] = v.x, x[2 * i + 1] = v.y;
+                top = max(top, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu));
+            }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = max(static_cast<int>(top >> 23) - 127, -100);  // floor(log2(largest)); 128: inf or NaN
-            const float down = __int_as_float((14 - ex + 127) << 23);
-            pow = __int_as_float((ex - 14 + 127) << 23);
+            const float up = __int_as_float((21 - ex + 127) << 23);
+            const float pow = ex == 128 ? __int_as_float(0x7fc00000) : __int_as_float((ex - 21 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < DH / 16; ++i) {
+                uint32_t d[3] = {0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int q = __float2int_rn(x[4 * i + j] * up);
+                    const int lo = static_cast<int8_t>(q), q1 = (q - lo) >> 8;
+                    const int mid = static_cast<int8_t>(q1), hi = (q1 - mid) >> 8;
+                    d[0] |= static_cast<uint32_t>(hi & 0xff) << (8 * j);
+                    d[1] |= static_cast<uint32_t>(mid & 0xff) << (8 * j);
+                    d[2] |= static_cast<uint32_t>(lo & 0xff) << (8 * j);
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) qb[nt][k * (DH / 16) + i] = d[k];
+            }
+            // score columns of this lane: 2 quad, 2 quad + 1 (rows of lanes 8 quad, 8 quad + 4 above)
+            q_pow[nt][0] = __shfl_sync(0xffffffffu, pow, 8 * quad) * p.scale_log2;
+            q_pow[nt][1] = __shfl_sync(0xffffffffu, pow, 8 * quad + 4) * p.scale_log2;
+        } else {
+            // k-step kk covers dims kk*16 .. +15
 #pragma unroll
             for (int kk = 0; kk < kKS; ++kk)
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    const float2 v = unpack16<true>(qb[nt][kk][ch]);
-                    qb[nt][kk][ch] = pack2<false>(v.x * down, v.y * down);
-                }
+                for (int ch = 0; ch < 2; ++ch)
+                    qb[nt][kk * 2 + ch] = h < heads ? q32[(kk * 16 + ch * 8 + 2 * quad) >> 1] : 0u;
         }
-        // score columns of this lane: 2 quad, 2 quad + 1 (rows of lanes 8 quad, 8 quad + 4 above)
-        q_pow[nt][0] = __shfl_sync(0xffffffffu, pow, 8 * quad) * p.scale_log2;
-        q_pow[nt][1] = __shfl_sync(0xffffffffu, pow, 8 * quad + 4) * p.scale_log2;
     }
     float slope[NT][2] = {};
     if constexpr (MOD) {
@@ -485,12 +492,19 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                             w[h][4 * c] = x.x, w[h][4 * c + 1] = x.y, w[h][4 * c + 2] = x.z, w[h][4 * c + 3] = x.w;
                         }
 #pragma unroll
-                    for (int kk = 0; kk < kKS; ++kk) {
-                        uint32_t a[4];
-                        s8x4_to_f16x2x2(w[0][kk], a[0], a[2]);
-                        s8x4_to_f16x2x2(w[1][kk], a[1], a[3]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        int acc[3][4] = {};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816<false>(sc[nt][mt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                        for (int kk = 0; kk < DH / 32; ++kk) {
+                            const uint32_t a[4] = {w[0][2 * kk], w[1][2 * kk], w[0][2 * kk + 1], w[1][2 * kk + 1]};
+#pragma unroll
+                            for (int k = 0; k < 3; ++k)
+                                mma_16832_s8(acc[k], a, qb[nt][k * (DH / 16) + 2 * kk], qb[nt][k * (DH / 16) + 2 * kk + 1]);
+                        }
+                        // |hi|, |mid| sums are at most 2^21: 256 hi + mid is an exact int
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[nt][mt][e] = fmaf(static_cast<float>(acc[0][e] * 256 + acc[1][e]), 256.f, static_cast<float>(acc[2][e]));
                     }
                 } else {
 #pragma unroll
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         uint32_t a[4];
                         ldsm_x4(sK + (c >> 3) * C::kBoxB + swz<128>(t, c), a[0], a[1], a[2], a[3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816<kQBF16>(sc[nt][mt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_16816<kQBF16>(sc[nt][mt], a, qb[nt][kk * 2], qb[nt][kk * 2 + 1]);
                     }
                 }
             }
