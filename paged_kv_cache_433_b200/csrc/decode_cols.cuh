@@ -760,7 +760,8 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
 // (cuts[c]: sequence, KV head, pieces), whose pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: the
 // warps share out the heads of the row's group and, with fewer heads than warps, a head's pieces (a long row of a small
 // batch is cut into dozens); a lane sums Dh / 32 dims with the loads of a round of pieces issued before any is used,
-// relative to its warp's own maximum, and the warps of a head meet in shared memory.
+// relative to its warp's own maximum, and the warps of a head meet in shared memory. The host gives it few warps where
+// rows have few pieces (large CTAs are slow to start) and kCombineColsWarps where they have many.
 constexpr int kCombineColsWarps = 16;
 template <int DH>
 __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_kernel(
@@ -774,9 +775,9 @@ __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_ker
     const int4 cut = cuts[c];
     if (cut.x < 0) return;
     const int ns = cut.z;
-    const int wph = max(1, kCombineColsWarps / g);  // warps per head
+    const int warps = blockDim.x >> 5, wph = max(1, warps / g);  // warps per head
     auto slot = [&](int s) -> int64_t { return s == 0 ? 2LL * c + 1 : 2LL * (c + s); };
-    for (int h0 = 0; h0 < g; h0 += kCombineColsWarps) {  // one round unless the group has more heads than warps
+    for (int h0 = 0; h0 < g; h0 += warps) {  // one round unless the group has more heads than warps
         const int h = h0 + warp / wph, part = warp % wph;
         float m = -INFINITY, L = 0.f, acc[kD] = {};
         if (h < g) {

@@ -838,7 +838,9 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
                                    static_cast<const int32_t*>(p.plan), B, H_q, H_kv);
         if (e != cudaSuccess) return KV_ERR_CUDA;
     } else if (cols.balanced) {
-        const dim3 blocks(static_cast<unsigned>(cols.grid)), threads(32 * kCombineColsWarps);
+        // pieces per row on average: many only for few long rows
+        const bool long_rows = cols.grid > 4 * static_cast<int64_t>(B) * H_kv;
+        const dim3 blocks(static_cast<unsigned>(cols.grid)), threads(32 * (long_rows ? kCombineColsWarps : 4));
         auto merge = [&](auto kernel) {
             return launch_pdl(kernel, blocks, threads, 0, st, out, p.part_u, p.part_ml,
                               static_cast<const int4*>(p.cuts), H_q, g);
