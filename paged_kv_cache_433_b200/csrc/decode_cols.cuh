@@ -236,14 +236,16 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
         if (threadIdx.x == 0) pre[0] = 0;
         __syncthreads();
         for (int bb = blockIdx.x; bb < p.B; bb += gridDim.x)  // rows without a visible page: no piece writes them
-            if (pre[bb + 1] == pre[bb])
+            if (pre[bb + 1] == pre[bb]) {
                 for (int e = threadIdx.x; e < p.H_q * DH; e += C::kThreads) p.out[(int64_t)bb * p.H_q * DH + e] = 0.f;
+                if (p.cuts_by_row && threadIdx.x < p.H_kv) p.cuts[bb * p.H_kv + threadIdx.x] = make_int4(-1, 0, 0, 0);
+            }
         T = pre[p.B] * p.H_kv;
         constexpr int kMin = kColsMinTokens / P;
         G = min(static_cast<int>(gridDim.x), (T + kMin - 1) / kMin);
         const int c = blockIdx.x;
         if (c >= G) {
-            if (threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
+            if (threadIdx.x == 0 && !p.cuts_by_row) p.cuts[c] = make_int4(-1, 0, 0, 0);
             return;
         }
         // positions floor(c T / G) .. floor((c + 1) T / G) (without 64-bit divisions: G^2 fits an int)
@@ -276,6 +278,11 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
         bool ok = true;
         int issued = 0;
         while (ok && walk.next(pc)) {
+            if (p.cuts_by_row && lane == 0 && (pc.slot & 1)) {  // the row starts here: whole (-1) or cut (2c + 1)
+                const int64_t after = pre[pc.b] * p.H_kv + static_cast<int64_t>(pc.kvh + 1) * (pre[pc.b + 1] - pre[pc.b]);
+                const int c = blockIdx.x, pieces = static_cast<int>((after * G - 1) / T) - c + 1;
+                p.cuts[pc.b * p.H_kv + pc.kvh] = make_int4(pc.slot < 0 ? -1 : pc.b, pc.kvh, pieces, c);
+            }
             const int n_units = (pc.tokens(P) + C::kU - 1) / C::kU, n_st = (n_units + kUPS - 1) / kUPS;
             const int32_t* row = p.block_tables + (int64_t)pc.b * p.max_blocks + pc.page0;
             int tab = 0;  // block-table entry of page (first page of the group & ~31) + lane
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
             }
             gs += n_st;
         }
-        if (balanced && lane == 0) {
+        if (balanced && !p.cuts_by_row && lane == 0) {
             // the row that holds this CTA's last position: does it start here (its first real page, that is) and run on?
             int4 cut = make_int4(-1, 0, 0, 0);
             const int pos0 = walk.start, last = walk.end - 1;
@@ -345,7 +352,8 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
             const int D = pre[b + 1] - pre[b], kvh = (last - pre[b] * p.H_kv) / D, start = pre[b] * p.H_kv + kvh * D;
             if (walk.end < start + D && walk.end > start + v && pos0 <= start + v) {
                 const int64_t after = static_cast<int64_t>(start) + D;  // the CTA of position after - 1 has the last piece
-                cut = make_int4(b, kvh, static_cast<int>((after * G - 1) / T) - static_cast<int>(blockIdx.x) + 1, 0);
+                cut = make_int4(b, kvh, static_cast<int>((after * G - 1) / T) - static_cast<int>(blockIdx.x) + 1,
+                                blockIdx.x);
             }
             p.cuts[blockIdx.x] = cut;
         }
@@ -756,8 +764,8 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
     }
 }
 
-// Merges the rows that a balanced launch cut: CTA c takes the row that starts in CTA c's range and runs past its end
-// (cuts[c]: sequence, KV head, pieces), whose pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: the
+// Merges the rows that a balanced launch cut, one CTA per entry of `cuts` (sequence, KV head, pieces, first CTA c): a
+// row's pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: the
 // warps share out the heads of the row's group and, with fewer heads than warps, a head's pieces (a long row of a small
 // batch is cut into dozens); a lane sums Dh / 32 dims with the loads of a round of pieces issued before any is used,
 // relative to its warp's own maximum, and the warps of a head meet in shared memory. The host gives it few warps where
@@ -771,10 +779,10 @@ __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_ker
     __shared__ float red_u[kCombineColsWarps][DH], red_m[kCombineColsWarps], red_l[kCombineColsWarps];
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 cut = cuts[c];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 cut = cuts[blockIdx.x];
     if (cut.x < 0) return;
-    const int ns = cut.z;
+    const int ns = cut.z, c = cut.w;
     const int warps = blockDim.x >> 5, wph = max(1, warps / g);  // warps per head
     auto slot = [&](int s) -> int64_t { return s == 0 ? 2LL * c + 1 : 2LL * (c + s); };
     for (int h0 = 0; h0 < g; h0 += warps) {  // one round unless the group has more heads than warps

@@ -75,7 +75,8 @@ struct DecodeParams {
     int32_t g, HS, WP;          // GQA group, head slices, page-warps
     int32_t num_splits, pages_per_split;
     float scale_log2;           // scale * log2(e)
-    int4* cuts;                 // heads-as-columns kernel, balanced: the row cut by each CTA's end
+    int4* cuts;                 // heads-as-columns kernel, balanced: {sequence, KV head, pieces, first CTA} of cut rows
+    int32_t cuts_by_row;        // 1: an entry per row (few rows), 0: an entry per CTA, for the row its end cuts
     const float* kv_scales;     // int8 K/V: [num_pages][H_kv][2][P] (K then V)
     // modified scores and masks (score_mod.cuh)
     float cap_in, cap_out;      // tanh cap c (cap_out = 0: none): scale / c and c * log2(e)

@@ -429,6 +429,7 @@ struct DecodeExtra {
 // too large for the CTAs' plan takes the grid rule of resolve_splits.
 struct ColsLayout {
     bool balanced = false;
+    bool by_row = false;  // fewer rows than a quarter of the CTAs: rows have many pieces, and an entry of the cuts each
     int32_t S = 1, C = 1, grid = 0;
     size_t ml_off = 0, u_off = 0, bytes = 0;  // balanced: the cuts come first
 };
@@ -455,6 +456,7 @@ int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_bl
     if (num_splits == 0 && !direct && !one_wave && B <= kColsMaxB && line < (1LL << 31)) {
         L.balanced = true;
         L.grid = static_cast<int32_t>(std::min<int64_t>(slots, (line + min_pages - 1) / min_pages));
+        L.by_row = 4LL * B * H_kv < L.grid;
         L.ml_off = sizeof(int4) * static_cast<size_t>(L.grid);
         L.u_off = (L.ml_off + sizeof(float2) * 2 * static_cast<size_t>(L.grid) * g + 15) / 16 * 16;
         L.bytes = L.u_off + sizeof(float) * 2 * static_cast<size_t>(L.grid) * g * Dh;
@@ -738,6 +740,7 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
         if (cols.balanced) {
             p.stream_plan = 1;
             p.cuts = reinterpret_cast<int4*>(w);
+            p.cuts_by_row = cols.by_row ? 1 : 0;
             grid = dim3(static_cast<unsigned>(cols.grid), 1, 1);
         }
     } else if (planned && tc) {
@@ -838,9 +841,8 @@ int decode_impl(float* out, const void* q, const void* k_new, const void* v_new,
                                    static_cast<const int32_t*>(p.plan), B, H_q, H_kv);
         if (e != cudaSuccess) return KV_ERR_CUDA;
     } else if (cols.balanced) {
-        // pieces per row on average: many only for few long rows
-        const bool long_rows = cols.grid > 4 * static_cast<int64_t>(B) * H_kv;
-        const dim3 blocks(static_cast<unsigned>(cols.grid)), threads(32 * (long_rows ? kCombineColsWarps : 4));
+        const dim3 blocks(static_cast<unsigned>(cols.by_row ? static_cast<int64_t>(B) * H_kv : cols.grid));
+        const dim3 threads(32 * (cols.by_row ? kCombineColsWarps : 4));
         auto merge = [&](auto kernel) {
             return launch_pdl(kernel, blocks, threads, 0, st, out, p.part_u, p.part_ml,
                               static_cast<const int4*>(p.cuts), H_q, g);
