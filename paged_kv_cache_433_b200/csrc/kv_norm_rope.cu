@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -208,6 +209,18 @@ __global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas) kv_norm_rope_
     }
 }
 
+// SMs of the current device (looked up once per device).
+int sm_count_cached() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    int v = cached[dev & 63].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    cached[dev & 63].store(v, std::memory_order_relaxed);
+    return v;
+}
+
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -275,10 +288,8 @@ extern "C" int kv_norm_rope_append(void* k_pages, void* v_pages, void* q_out, vo
     const int64_t units = (static_cast<int64_t>(p.q_rows) + H_kv + (cache ? H_kv : 0)) * (vpr / 2);
     if (units > 0x7fffffffLL) return KV_ERR_UNSUPPORTED;
     const int threads = static_cast<int>(std::min<int64_t>(kNormRopeThreads, (units + 31) / 32 * 32));
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return KV_ERR_CUDA;
+    const int sms = sm_count_cached();
+    if (sms <= 0) return KV_ERR_CUDA;
     const int64_t blocks = std::min<int64_t>(B, static_cast<int64_t>(sms) * std::max(1, kNormRopeThreads * kNormRopeCtas / threads));  // resident CTAs
     auto run = [&](auto kernel) {
         return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, static_cast<cudaStream_t>(stream),

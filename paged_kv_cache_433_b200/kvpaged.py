@@ -450,8 +450,8 @@ def paged_prefill_attention(out, q, q_start, max_q_len: int, k_pages, v_pages, b
 
 
 # ---- per-head norm + rotation + append, int8 cache, modified scores and masks
-# A decode step makes these calls once per layer and the GPU's part of a small one is a few microseconds, so the checks
-# of a tensor are one function call, and only a failed check looks for its reason.
+# A decode step makes these calls once per layer, and the GPU's part of a small one is a few microseconds: an entry point
+# checks its tensors in one expression, and only where that fails does _refuse look for the tensor and the reason.
 _torch = None  # the torch module, once a device call has imported it
 
 
@@ -473,38 +473,36 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _refuse(t, name: str, shape, dtype):
-    if t is None or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.get_device() != _torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    raise ValueError(f"{name} must be contiguous (within a token's heads, where tokens may be strided)")
+def _refuse(dev: int, *specs) -> None:
+    """Raises for the first of the tensors (tensor, name, shape, dtype[, tokens strided]) that is not as it has to be."""
+    for t, name, shape, dtype, *strided in specs:
+        if t is None or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device")
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
-def _at(t, dev: int, name: str, shape, dtype) -> int:
-    """Pointer of a contiguous tensor of this shape and dtype on device `dev`."""
-    if t is None or t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(t, name, shape, dtype)
+def _at(t, dev: int, name: str, shape, dtype):
+    """Pointer of a contiguous tensor of this shape and dtype on device `dev` (None passes through)."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(dev, (t, name, shape, dtype))
     return t.data_ptr()
 
 
-def _at_or_none(t, dev: int, name: str, shape, dtype):
-    return None if t is None else _at(t, dev, name, shape, dtype)
-
-
-def _tokens_at(t, dev: int, name: str, shape, dtype):
-    """(pointer, elements from token to token) of a [B, H, Dh] tensor whose heads are contiguous within a token."""
-    if t is None or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
-        _refuse(t, name, shape, dtype)
+def _token_stride(t, name: str, H: int, Dh: int) -> int:
+    """Elements from token to token of a [B, H, Dh] tensor whose heads are contiguous within a token."""
     st, sh, sd = t.stride()
-    B, H, Dh = shape
     if (sd != 1 and Dh != 1) or (sh != Dh and H != 1):
-        _refuse(t, name, shape, dtype)
-    return t.data_ptr(), (st if B > 1 else H * Dh)
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if t.shape[0] > 1 else H * Dh
 
 
 def _flag_at(err_flag, dev: int):
@@ -517,7 +515,7 @@ def _flag_at(err_flag, dev: int):
 def _scratch_at(workspace, dev: int):
     if workspace is None:
         return None, 0
-    return _at(workspace, dev, "workspace", workspace.shape, workspace.dtype), workspace.numel() * workspace.element_size()
+    return _at(workspace, dev, "workspace", workspace.shape, workspace.dtype), workspace.nbytes
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -535,39 +533,58 @@ def kv_norm_rope_append(k_pages, v_pages, k_new, v_new, slot_mapping, positions,
     projection's output); q_out, k_out contiguous. k/v_pages, v_new and slot_mapping may be None together when k_out
     is given (a quantising append writes the cache then). Other arguments as kv_rope_append."""
     dev = _begin(k_new, "k_new")
-    dt, f32 = k_new.dtype, _torch.float32
+    dt, f32, i32, i64 = k_new.dtype, _torch.float32, _torch.int32, _torch.int64
     kshape = B, H_kv, Dh = k_new.shape
     num_pages, kp, vp, vptr, vs, slots = 0, None, None, None, 0, None
     if k_pages is not None:
         num_pages = k_pages.shape[0]
         pshape = (num_pages, H_kv, page_size, Dh)
-        kp, vp = _at(k_pages, dev, "k_pages", pshape, dt), _at(v_pages, dev, "v_pages", pshape, dt)
-        vptr, vs = _tokens_at(v_new, dev, "v_new", kshape, dt)
-        slots = _at(slot_mapping, dev, "slot_mapping", (B,), _torch.int64)
+        if v_pages is None or v_new is None or slot_mapping is None or not (
+                k_pages.dtype == v_pages.dtype == v_new.dtype == dt and k_pages.shape == pshape and v_pages.shape == pshape
+                and v_new.shape == kshape and slot_mapping.shape == (B,) and slot_mapping.dtype == i64
+                and k_pages.get_device() == v_pages.get_device() == v_new.get_device() == slot_mapping.get_device() == dev
+                and k_pages.is_contiguous() and v_pages.is_contiguous() and slot_mapping.is_contiguous()):
+            _refuse(dev, (k_pages, "k_pages", pshape, dt), (v_pages, "v_pages", pshape, dt),
+                    (v_new, "v_new", kshape, dt, True), (slot_mapping, "slot_mapping", (B,), i64))
+        kp, vp, vptr, slots = k_pages.data_ptr(), v_pages.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr()
+        vs = _token_stride(v_new, "v_new", H_kv, Dh)
     else:
         _need(v_pages is None and v_new is None and slot_mapping is None, "v_pages, v_new and slot_mapping need k_pages")
-    kptr, ks = _tokens_at(k_new, dev, "k_new", kshape, dt)
+    max_pos = cos_sin.shape[0]
+    if not (positions.shape == (B,) and positions.dtype == i32 and cos_sin.shape == (max_pos, Dh) and cos_sin.dtype == f32
+            and positions.get_device() == cos_sin.get_device() == dev and positions.is_contiguous()
+            and cos_sin.is_contiguous()):
+        _refuse(dev, (positions, "positions", (B,), i32), (cos_sin, "cos_sin", (max_pos, Dh), f32))
     _need((q is None) == (q_out is None), "q and q_out go together")
     H_q, qptr, qs, qo = 0, None, 0, None
     if q is not None:
         H_q = q.shape[1]
-        qptr, qs = _tokens_at(q, dev, "q", (B, H_q, Dh), dt)
-        qo = _at(q_out, dev, "q_out", (B, H_q, Dh), dt)
-    max_pos = cos_sin.shape[0]
+        qshape = (B, H_q, Dh)
+        if not (q.shape == qshape and q_out.shape == qshape and q.dtype == q_out.dtype == dt
+                and q.get_device() == q_out.get_device() == dev and q_out.is_contiguous()):
+            _refuse(dev, (q, "q", qshape, dt, True), (q_out, "q_out", qshape, dt))
+        qptr, qo, qs = q.data_ptr(), q_out.data_ptr(), _token_stride(q, "q", H_q, Dh)
     rc = lib().kv_norm_rope_append(
-        kp, vp, qo, _at_or_none(k_out, dev, "k_out", kshape, dt), qptr, kptr, vptr, qs, ks, vs,
-        _at_or_none(q_weight, dev, "q_weight", (Dh,), f32), _at_or_none(k_weight, dev, "k_weight", (Dh,), f32), float(eps), slots,
-        _at(positions, dev, "positions", (B,), _torch.int32), _at(cos_sin, dev, "cos_sin", (max_pos, Dh), f32), max_pos,
+        kp, vp, qo, _at(k_out, dev, "k_out", kshape, dt), qptr, k_new.data_ptr(), vptr, qs,
+        _token_stride(k_new, "k_new", H_kv, Dh), vs, _at(q_weight, dev, "q_weight", (Dh,), f32),
+        _at(k_weight, dev, "k_weight", (Dh,), f32), float(eps), slots, positions.data_ptr(), cos_sin.data_ptr(), max_pos,
         ROPE_STYLE[style], B, H_q, H_kv, Dh, page_size, num_pages, _torch_dtype_code(k_new), _flag_at(err_flag, dev),
         _raw_stream(stream, dev))
-    _check("kv_norm_rope_append", rc)
+    if rc:
+        _check("kv_norm_rope_append", rc)
 
 
 def _int8_pools_at(k_pages, v_pages, kv_scales, dev: int):
     """Shape and pointers of int8 pools [num_pages, H_kv, P, Dh] and their scales [num_pages, H_kv, 2, P]."""
     shape = num_pages, H_kv, P, _ = k_pages.shape
-    return (shape, _at(k_pages, dev, "k_pages", shape, _torch.int8), _at(v_pages, dev, "v_pages", shape, _torch.int8),
-            _at(kv_scales, dev, "kv_scales", (num_pages, H_kv, 2, P), _torch.float32))
+    i8, f32 = _torch.int8, _torch.float32
+    if v_pages is None or kv_scales is None or not (
+            k_pages.dtype == v_pages.dtype == i8 and v_pages.shape == shape and kv_scales.dtype == f32
+            and kv_scales.shape == (num_pages, H_kv, 2, P) and v_pages.get_device() == kv_scales.get_device() == dev
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and kv_scales.is_contiguous()):
+        _refuse(dev, (k_pages, "k_pages", shape, i8), (v_pages, "v_pages", shape, i8),
+                (kv_scales, "kv_scales", (num_pages, H_kv, 2, P), f32))
+    return shape, k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr()
 
 
 def kv_append_int8(k_pages, v_pages, kv_scales, k_new, v_new, slot_mapping, page_size: int, err_flag=None,
@@ -578,12 +595,26 @@ def kv_append_int8(k_pages, v_pages, kv_scales, k_new, v_new, slot_mapping, page
     (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
     _need(P == page_size, "the pools' page size differs")
     dt, B = k_new.dtype, k_new.shape[0]
-    kptr, ks = _tokens_at(k_new, dev, "k_new", (B, H_kv, Dh), dt)
-    vptr, vs = _tokens_at(v_new, dev, "v_new", (B, H_kv, Dh), dt)
-    rc = lib().kv_append_int8(kp, vp, sc, kptr, vptr, ks, vs, _torch_dtype_code(k_new),
-                              _at(slot_mapping, dev, "slot_mapping", (B,), _torch.int64), B, H_kv, Dh, P, num_pages,
-                              _flag_at(err_flag, dev), _raw_stream(stream, dev))
-    _check("kv_append_int8", rc)
+    shape = (B, H_kv, Dh)
+    if not (k_new.shape == shape and v_new.shape == shape and v_new.dtype == dt and slot_mapping.shape == (B,)
+            and slot_mapping.dtype == _torch.int64 and slot_mapping.is_contiguous()
+            and k_new.get_device() == v_new.get_device() == slot_mapping.get_device() == dev):
+        _refuse(dev, (k_new, "k_new", shape, dt, True), (v_new, "v_new", shape, dt, True),
+                (slot_mapping, "slot_mapping", (B,), _torch.int64))
+    rc = lib().kv_append_int8(kp, vp, sc, k_new.data_ptr(), v_new.data_ptr(), _token_stride(k_new, "k_new", H_kv, Dh),
+                              _token_stride(v_new, "v_new", H_kv, Dh), _torch_dtype_code(k_new), slot_mapping.data_ptr(), B,
+                              H_kv, Dh, P, num_pages, _flag_at(err_flag, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("kv_append_int8", rc)
+
+
+def _page_lists(src_pages, dst_pages, dev: int) -> int:
+    n, i32 = src_pages.numel(), _torch.int32
+    if not (src_pages.shape == (n,) and dst_pages.shape == (n,) and src_pages.dtype == dst_pages.dtype == i32
+            and src_pages.get_device() == dst_pages.get_device() == dev and src_pages.is_contiguous()
+            and dst_pages.is_contiguous()):
+        _refuse(dev, (src_pages, "src_pages", (n,), i32), (dst_pages, "dst_pages", (n,), i32))
+    return n
 
 
 def kv_dequant_pages_int8(k_out, v_out, k_pages, v_pages, kv_scales, src_pages, dst_pages, err_flag=None,
@@ -594,23 +625,24 @@ def kv_dequant_pages_int8(k_out, v_out, k_pages, v_pages, kv_scales, src_pages, 
     (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
     num_out, dt = k_out.shape[0], k_out.dtype
     oshape = (num_out, H_kv, P, Dh)
-    n = src_pages.numel()
+    n = _page_lists(src_pages, dst_pages, dev)
     rc = lib().kv_dequant_pages_int8(
         _at(k_out, dev, "k_out", oshape, dt), _at(v_out, dev, "v_out", oshape, dt), _torch_dtype_code(k_out), num_out, kp, vp,
-        sc, _at(src_pages, dev, "src_pages", (n,), _torch.int32), _at(dst_pages, dev, "dst_pages", (n,), _torch.int32), n, H_kv,
-        Dh, P, num_pages, _flag_at(err_flag, dev), _raw_stream(stream, dev))
-    _check("kv_dequant_pages_int8", rc)
+        sc, src_pages.data_ptr(), dst_pages.data_ptr(), n, H_kv, Dh, P, num_pages, _flag_at(err_flag, dev),
+        _raw_stream(stream, dev))
+    if rc:
+        _check("kv_dequant_pages_int8", rc)
 
 
 def kv_copy_pages_int8(k_pages, v_pages, kv_scales, src_pages, dst_pages, err_flag=None, stream=None) -> None:
     """kv_copy_pages of int8 pools: codes and scales of pages src_pages[i] -> dst_pages[i] (int32, device)."""
     dev = _begin(k_pages, "k_pages")
     (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
-    n = src_pages.numel()
-    rc = lib().kv_copy_pages_int8(kp, vp, sc, _at(src_pages, dev, "src_pages", (n,), _torch.int32),
-                                  _at(dst_pages, dev, "dst_pages", (n,), _torch.int32), n, H_kv, Dh, P, num_pages,
+    n = _page_lists(src_pages, dst_pages, dev)
+    rc = lib().kv_copy_pages_int8(kp, vp, sc, src_pages.data_ptr(), dst_pages.data_ptr(), n, H_kv, Dh, P, num_pages,
                                   _flag_at(err_flag, dev), _raw_stream(stream, dev))
-    _check("kv_copy_pages_int8", rc)
+    if rc:
+        _check("kv_copy_pages_int8", rc)
 
 
 def paged_decode_ext_workspace_bytes(B: int, H_q: int, H_kv: int, Dh: int, max_blocks: int, page_size: int,
@@ -622,21 +654,45 @@ def paged_decode_ext_workspace_bytes(B: int, H_q: int, H_kv: int, Dh: int, max_b
     return out.value
 
 
+def _queries_at(out, q, q_dtype, block_tables, seq_lens, N: int, H_q: int, Dh: int, dev: int) -> tuple:
+    """Checks out fp32 [N, H_q, Dh], q of q_dtype, block_tables int32 [B, max_blocks] and seq_lens int32 [B]; returns
+    (B, max_blocks) and the pointers."""
+    B, mb = block_tables.shape
+    i32, f32, shape = _torch.int32, _torch.float32, (N, H_q, Dh)
+    if not (q.shape == shape and out.shape == shape and q.dtype == q_dtype and out.dtype == f32
+            and block_tables.dtype == seq_lens.dtype == i32 and seq_lens.shape == (B,) and out.is_contiguous()
+            and out.get_device() == q.get_device() == block_tables.get_device() == seq_lens.get_device() == dev
+            and q.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous()):
+        _refuse(dev, (out, "out", shape, f32), (q, "q", shape, q_dtype), (block_tables, "block_tables", (B, mb), i32),
+                (seq_lens, "seq_lens", (B,), i32))
+    return B, mb, out.data_ptr(), q.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr()
+
+
 def paged_decode_attention_int8(out, q, k_pages, v_pages, kv_scales, block_tables, seq_lens, scale: float,
                                 num_splits: int = 0, workspace=None, err_flag=None, stream=None) -> None:
     """Decode over int8 pools [num_pages, H_kv, P, Dh] with scales [num_pages, H_kv, 2, P]; q bf16/fp16 [B, H_q, Dh];
     other arguments as paged_decode_attention."""
     dev = _begin(k_pages, "k_pages")
     (num_pages, H_kv, P, Dh), kp, vp, sc = _int8_pools_at(k_pages, v_pages, kv_scales, dev)
-    B, H_q, _ = q.shape
-    mb = block_tables.shape[1]
+    N, H_q, _ = q.shape
+    B, mb, po, pq, pt, pl = _queries_at(out, q, q.dtype, block_tables, seq_lens, N, H_q, Dh, dev)
+    _need(N == B, "q must have a row per sequence")
     ws, ws_bytes = _scratch_at(workspace, dev)
-    rc = lib().paged_decode_attention_int8(
-        _at(out, dev, "out", (B, H_q, Dh), _torch.float32), _at(q, dev, "q", (B, H_q, Dh), q.dtype), _torch_dtype_code(q), kp,
-        vp, sc, _at(block_tables, dev, "block_tables", (B, mb), _torch.int32), mb,
-        _at(seq_lens, dev, "seq_lens", (B,), _torch.int32), B, H_q, H_kv, Dh, P, num_pages, float(scale), num_splits, ws, ws_bytes,
-        _flag_at(err_flag, dev), _raw_stream(stream, dev))
-    _check("paged_decode_attention_int8", rc)
+    rc = lib().paged_decode_attention_int8(po, pq, _torch_dtype_code(q), kp, vp, sc, pt, mb, pl, B, H_q, H_kv, Dh, P,
+                                           num_pages, float(scale), num_splits, ws, ws_bytes, _flag_at(err_flag, dev),
+                                           _raw_stream(stream, dev))
+    if rc:
+        _check("paged_decode_attention_int8", rc)
+
+
+def _pools16_at(k_pages, v_pages, dev: int):
+    """Shape and pointers of pools [num_pages, H_kv, P, Dh] of one dtype."""
+    shape, dt = k_pages.shape, k_pages.dtype
+    if v_pages is None or not (v_pages.shape == shape and v_pages.dtype == dt and len(shape) == 4 and k_pages.is_contiguous()
+                               and v_pages.is_contiguous() and v_pages.get_device() == dev):
+        _need(len(shape) == 4, "the pools must be [num_pages, H_kv, P, Dh]")
+        _refuse(dev, (k_pages, "k_pages", shape, dt), (v_pages, "v_pages", shape, dt))
+    return shape, k_pages.data_ptr(), v_pages.data_ptr()
 
 
 def paged_decode_attention_mod(out, q, k_pages, v_pages, block_tables, seq_lens, scale: float, softcap: float = 0.0,
@@ -645,20 +701,18 @@ def paged_decode_attention_mod(out, q, k_pages, v_pages, block_tables, seq_lens,
     """paged_decode_attention (bf16/fp16 pools) with capped scores (softcap > 0), a distance bias (alibi_slopes fp32
     [H_q]), a sliding window (window > 0) and a first visible key per sequence (key_start int32 [B])."""
     dev = _begin(k_pages, "k_pages")
-    pshape = num_pages, H_kv, P, Dh = k_pages.shape
-    dt, i32 = k_pages.dtype, _torch.int32
-    B, H_q, _ = q.shape
-    mb = block_tables.shape[1]
+    (num_pages, H_kv, P, Dh), kp, vp = _pools16_at(k_pages, v_pages, dev)
+    N, H_q, _ = q.shape
+    B, mb, po, pq, pt, pl = _queries_at(out, q, k_pages.dtype, block_tables, seq_lens, N, H_q, Dh, dev)
+    _need(N == B, "q must have a row per sequence")
     ws, ws_bytes = _scratch_at(workspace, dev)
     rc = lib().paged_decode_attention_mod(
-        _at(out, dev, "out", (B, H_q, Dh), _torch.float32), _at(q, dev, "q", (B, H_q, Dh), dt),
-        _at(k_pages, dev, "k_pages", pshape, dt), _at(v_pages, dev, "v_pages", pshape, dt),
-        _at(block_tables, dev, "block_tables", (B, mb), i32), mb, _at(seq_lens, dev, "seq_lens", (B,), i32), B, H_q, H_kv, Dh,
-        P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
-        _at_or_none(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
-        _at_or_none(key_start, dev, "key_start", (B,), i32), num_splits, ws, ws_bytes, _flag_at(err_flag, dev),
+        po, pq, kp, vp, pt, mb, pl, B, H_q, H_kv, Dh, P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
+        _at(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
+        _at(key_start, dev, "key_start", (B,), _torch.int32), num_splits, ws, ws_bytes, _flag_at(err_flag, dev),
         _raw_stream(stream, dev))
-    _check("paged_decode_attention_mod", rc)
+    if rc:
+        _check("paged_decode_attention_mod", rc)
 
 
 def paged_prefill_attention_mod(out, q, q_start, max_q_len: int, k_pages, v_pages, block_tables, seq_lens, scale: float,
@@ -667,19 +721,18 @@ def paged_prefill_attention_mod(out, q, q_start, max_q_len: int, k_pages, v_page
     """paged_prefill_attention with the score and mask options of paged_decode_attention_mod (key_start int32 [N], one
     per row) and a bidirectional prefix per sequence (prefix_lens int32 [B])."""
     dev = _begin(k_pages, "k_pages")
-    pshape = num_pages, H_kv, P, Dh = k_pages.shape
-    dt, i32 = k_pages.dtype, _torch.int32
+    (num_pages, H_kv, P, Dh), kp, vp = _pools16_at(k_pages, v_pages, dev)
     N, H_q, _ = q.shape
-    B, mb = block_tables.shape
+    B, mb, po, pq, pt, pl = _queries_at(out, q, k_pages.dtype, block_tables, seq_lens, N, H_q, Dh, dev)
+    i32 = _torch.int32
     rc = lib().paged_prefill_attention_mod(
-        _at(out, dev, "out", (N, H_q, Dh), _torch.float32), _at(q, dev, "q", (N, H_q, Dh), dt),
-        _at(q_start, dev, "q_start", (B + 1,), i32), int(max_q_len), _at(k_pages, dev, "k_pages", pshape, dt),
-        _at(v_pages, dev, "v_pages", pshape, dt), _at(block_tables, dev, "block_tables", (B, mb), i32), mb,
-        _at(seq_lens, dev, "seq_lens", (B,), i32), B, H_q, H_kv, Dh, P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
-        _at_or_none(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
-        _at_or_none(key_start, dev, "key_start", (N,), i32), _at_or_none(prefix_lens, dev, "prefix_lens", (B,), i32),
+        po, pq, _at(q_start, dev, "q_start", (B + 1,), i32), int(max_q_len), kp, vp, pt, mb, pl, B, H_q, H_kv, Dh, P,
+        num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
+        _at(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
+        _at(key_start, dev, "key_start", (N,), i32), _at(prefix_lens, dev, "prefix_lens", (B,), i32),
         _flag_at(err_flag, dev), _raw_stream(stream, dev))
-    _check("paged_prefill_attention_mod", rc)
+    if rc:
+        _check("paged_prefill_attention_mod", rc)
 
 
 KV_DECODE_KERNEL_AUTO, KV_DECODE_KERNEL_SIMT, KV_DECODE_KERNEL_MMA, KV_DECODE_KERNEL_TCGEN05 = 0, 1, 2, 3
