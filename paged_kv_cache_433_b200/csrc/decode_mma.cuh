@@ -457,8 +457,9 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     const float sl2 = kFP8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
     bool ok = true;
 
-    // MOD: earlier accumulations are summed in the output rows (kFlushKeys, score_mod.cuh); a thread
-    // reads back what it wrote itself (q_tile * g rows take three or four 16-row slices: one warp per row)
+    // MOD: earlier accumulations are summed in the output rows (kFlushKeys, score_mod.cuh); a thread reads back what it
+    // wrote itself. Only where one warp has the whole row: the host gives a row to several (WP > 1) only when that many
+    // times kFlushKeys hold all keys.
     constexpr int kFlush = kFlushKeys / C::kTP;
     bool flushed = false;
     float sum_scale[2] = {1.f, 1.f};
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
         const int n_st = (n_local + PPS - 1) / PPS;
         for (int i = wp; i < n_st; i += p.WP) {
             if constexpr (MOD) {
-                if (i > 0 && i % kFlush == 0) {
+                if (p.WP == 1 && i > 0 && i % kFlush == 0) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (r0 + 8 * h < rows) {
