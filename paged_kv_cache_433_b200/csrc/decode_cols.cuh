@@ -4,17 +4,21 @@
 //
 // Same contract and the same online (m, l, u) merge as decode_mma.cuh
 // ("07｜KV Cache、FlashAttention与PagedAttention的内部过程", Q027), with the two
-// contractions of a stage of TP = 32 tokens transposed:
-//   S^T[TP x 8 NT]  = K[TP x Dh] . Q^T[Dh x 8 NT]     (m16n8k16, k over dims)
+// contractions of a stage of TP tokens (16; int8: 32) transposed:
+//   S^T[TP x 8 NT]  = K[TP x Dh] . Q^T[Dh x 8 NT]     (k over dims)
 //   O^T[Dh x 8 NT] += V^T[Dh x TP] . P^T[TP x 8 NT]   (m16n8k16, k over tokens)
 // A GQA group of up to 8 heads fills an MMA's 8 columns, where it would fill
 // half of the 16 rows: half the MMAs, and half the registers of Q and of the
 // output, so that three CTAs of four consumer warps run on an SM. That
-// matters most for int8: a stage costs about 900 instructions there (the codes
-// are widened with integer operations), far from what one warp scheduler
-// issues but with few warps bound by their latencies (8B-shaped layer, B = 64:
-// rows as heads 81 us, 8 consumer warps an SM, 0.45 instructions a cycle and
-// scheduler).
+// matters most for int8, whose warps are bound by latencies: 64 sequences of
+// 512..4096 tokens of an 8B-shaped layer (32 heads on 8, Dh = 128) took 81 us
+// with heads as rows and 8 consumer warps an SM, and take 61 us.
+//
+// int8: the K codes are the first product's operand as they are (m16n8k32 of
+// signed bytes, 32-bit sums, exact); a query row, behind a power of two, is an
+// integer of 23 bits split into three signed bytes, an MMA each. The V codes
+// are widened to bf16, which holds them exactly, and their scales multiply the
+// probabilities.
 //
 // Probabilities go into the second product as a 16-bit value plus its rounded
 // residual. Their fragment (token rows, head columns) becomes the second
@@ -38,7 +42,15 @@
 // page's rows x 128 bytes with 128-byte swizzle (64 for int8 rows of 64
 // bytes; at most 16 rows for 16-bit pages), a ring of stages; int8 scales are
 // one bulk copy per (page, head). Pages outside the pool are skipped one by
-// one (KV_DEV_ERR_PAGE_RANGE). Bound by HBM where the batch fills the machine.
+// one (KV_DEV_ERR_PAGE_RANGE).
+//
+// Measured (8B-shaped layer, time of the whole call on the GPU, of the measured
+// copy rate): 16-bit, capped, 64 sequences of 512..4096 tokens 69 us, 5.77 TB/s
+// (0.88); 256 of 16..8192 with document masks and a distance bias 66 us (0.77,
+// the lengths' spread and the merge); int8, those 64: 61 us, 4.25 TB/s (0.65:
+// its loads alone take 47 us; scales, integer products and widening share the
+// issue slots); int8, one sequence of 32768: 26 us (0.40: 444 CTAs' start and
+// the merge of one row's 55 pieces).
 #pragma once
 
 #include <cuda.h>
@@ -52,11 +64,9 @@
 namespace kvp {
 
 constexpr int kColsMaxB = 1024;      // sequences of a balanced launch
-#ifndef KVP_CW
-#define KVP_CW 4
-#define KVP_CC 3
-#endif
-constexpr int kColsWarps1 = KVP_CW, kColsCtas1 = KVP_CC;  // groups of at most 8 heads: consumer warps per CTA, CTAs per SM
+// Groups of at most 8 heads: consumer warps per CTA, CTAs per SM (8B-shaped layer, int8, 64 sequences of 512..4096
+// tokens: 68 us when 2 CTAs of 7 warps took 77, 2 of 6 72, 4 of 3 74.5, one of 15 97).
+constexpr int kColsWarps1 = 4, kColsCtas1 = 3;
 constexpr int kColsItemTokens = 128; // a row's fixed cost in tokens (its queries, its merge)
 constexpr int kColsMinTokens = 128;  // at least one stage per consumer warp and CTA
 
@@ -612,7 +622,16 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                 }
             }
 
-            // ---- O^T += V^T P^T
+            // ---- O^T += V^T P^T: sixteen tokens a product, added to fp32 sums. (Sums kept in the MMA's accumulator,
+            // which rounds towards zero, cost the same time and grow less exact with the length: score_mod.cuh.)
+            auto add_pv = [&](float(&sum)[4], const uint32_t(&a)[4], const uint32_t(&hi)[2], const uint32_t(&lo)[2]) {
+                float d[4] = {};
+                mma_16816<kPBF16>(d, a, hi[0], hi[1]);
+                if constexpr (!DUP) mma_16816<kPBF16>(d, a, lo[0], lo[1]);
+                const float2 x = fadd2(make_float2(sum[0], sum[1]), make_float2(d[0], d[1]));
+                const float2 y = fadd2(make_float2(sum[2], sum[3]), make_float2(d[2], d[3]));
+                sum[0] = x.x, sum[1] = x.y, sum[2] = y.x, sum[3] = y.y;
+            };
 #pragma unroll
             for (int ks = 0; ks < kMT; ++ks) {
                 if constexpr (kI8) {
@@ -640,10 +659,8 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                             s8x4_to_bf16x2x2(byte_perm(wv[0][m], wv[1][m], sel), a[0], a[1]);
                             s8x4_to_bf16x2x2(byte_perm(wv[2][m], wv[3][m], sel), a[2], a[3]);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma_16816<true>(o[nt][2 * m + hh], a, ph[nt][ks][0], ph[nt][ks][1]);
-                                if constexpr (!DUP) mma_16816<true>(o[nt][2 * m + hh], a, pl[nt][ks][0], pl[nt][ks][1]);
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+                                add_pv(o[nt][2 * m + hh], a, ph[nt][ks], pl[nt][ks]);
                         }
                 } else {
 #pragma unroll
@@ -652,10 +669,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         uint32_t a[4];
                         ldsm_x4_trans(sV + (c >> 3) * C::kBoxB + swz<128>(t, c), a[0], a[1], a[2], a[3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_16816<kPBF16>(o[nt][m], a, ph[nt][ks][0], ph[nt][ks][1]);
-                            if constexpr (!DUP) mma_16816<kPBF16>(o[nt][m], a, pl[nt][ks][0], pl[nt][ks][1]);
-                        }
+                        for (int nt = 0; nt < NT; ++nt) add_pv(o[nt][m], a, ph[nt][ks], pl[nt][ks]);
                     }
                 }
             }

@@ -1029,10 +1029,11 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     if (mod) {
         set_mod(p, scale, mod->softcap, mod->alibi_slopes, mod->window, mod->key_start);
         p.prefix_lens = mod->prefix_lens;
-        // A cap bounds every score by cap_out; where 2^(2 cap_out) fits fp32's range with room for sums (bf16 operands
-        // have that range too) and no bias moves the scores, one reference serves all rows: no row maximum is taken.
+        // A cap bounds every score by cap_out; where 2^(2 cap_out) fits fp32's range with room on both sides (bf16
+        // operands have that range too) and no bias moves the scores, one reference serves all rows: no row maximum is
+        // taken.
         fixed_ref = dtype == KV_DTYPE_BF16 && mod->softcap > 0.f && p.cap_out <= kFixedRefMax && !mod->alibi_slopes;
-        p.fixed_ref = std::max(0.f, p.cap_out - 40.f);
+        p.fixed_ref = std::max(0.f, p.cap_out - kFixedTop);
     }
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;

@@ -14,7 +14,7 @@
 //   - A thread writes P over the S columns that it read itself, so that the two
 //     threads of a row meet only to move the row's reference maximum: they vote
 //     in one barrier whether any row has to, and exchange maxima only then.
-//   - FIXED (bf16, a cap of at most 55, no bias): the cap bounds the scores, one
+//   - FIXED (bf16, a cap of at most 50, no bias): the cap bounds the scores, one
 //     reference serves every row, and neither maximum nor barrier is needed; the
 //     reference is subtracted by the last multiply-add of the cap's polynomial.
 //     Three softmax warpgroups then work on different stages, one row per

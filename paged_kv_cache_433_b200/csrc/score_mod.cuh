@@ -75,8 +75,10 @@ constexpr double kTanhPoly[kCapTerms] = {0.999999971, -0.333329589, 0.13325406, 
 constexpr int kCapTinyTerms = 3;
 constexpr double kTanhTiny = 0.2;
 constexpr double kTanhTinyPoly[kCapTinyTerms] = {0.999999895, -0.333285909, 0.130154075};
-// Chunked prefill: the largest cap (log2 units) with one softmax reference for all rows.
-constexpr float kFixedRefMax = 80.f;
+// Chunked prefill: the largest cap (log2 units; 50 in natural ones) with one softmax reference for all rows, and the
+// largest power of two that its probabilities then reach: they lie in 2^-96 .. 2^50, a residual of 16-bit splitting 2^9
+// lower, so that sums with values from 1e-6 to 1e17 stay inside the normal range.
+constexpr float kFixedRefMax = 73.f, kFixedTop = 50.f;
 // The coefficients as packed pairs in registers: loaded once through volatile moves, or the compiler fetches both
 // halves of each again for every pair of scores (the packed operations take no constant-bank operand).
 struct CapCoef {
@@ -223,10 +225,13 @@ __device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCo
     }
 }
 
-// The tensor core rounds each sum of 16 products and the accumulator towards zero: over n keys an accumulator loses
-// about n 2^-29 of itself (8.4e-6 at 4224 keys, 6.5e-5 at 32K, measured with warp MMA and tcgen05 alike). The
-// multi-token kernels therefore move their output accumulators into fp32 sums, kept in the output rows that the same
-// threads write at the end, after every kFlushKeys keys.
+// The tensor core rounds each sum of 16 products and the accumulator towards zero. Over n keys an accumulator loses
+// about n 2^-29 of the result for values around zero (8.4e-6 at 4224 keys, 6.5e-5 at 32K, measured with warp MMA and
+// tcgen05 alike), and up to n / 8 times 2^-23 for values of one sign (1.0e-5 at 2048). The multi-token kernels
+// therefore move their output accumulators into fp32 sums after every kFlushKeys keys, in registers (tcgen05) or in the
+// output rows that the same threads write at the end (warp MMA). More often costs more than it gives: 8 chunks of 512
+// tokens over 4096, capped, 475 us at 2048 keys and 6.8e-6 off; 507 us at 1024 and 5.5e-6; 576 us at 512 and 5.1e-6
+// (the rest is the 16-bit splitting of the probabilities).
 constexpr int kFlushKeys = 2048;
 
 // ---- 16-bit values with an all-ones exponent (NaN, +-inf) -----------------
