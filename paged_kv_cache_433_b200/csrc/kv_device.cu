@@ -1041,8 +1041,12 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
         return KV_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>((max_q_len + q_tile - 1) / q_tile), static_cast<unsigned>(H_kv),
                     static_cast<unsigned>(B));
+    const int64_t n_tiles = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+    fixed_ref = fixed_ref && tc && n_tiles < (1LL << 31);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
+                          : fixed_ref              ? launch_prefill_cap_tc(p, tk, tv, page_size, static_cast<int>(grid.x),
+                                                                           static_cast<int>(n_tiles), st)
                           : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, fixed_ref, grid, st)
                           : tc                     ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
                           : dtype == KV_DTYPE_BF16 ? launch_prefill_bf16(p, tk, tv, Dh, page_size, grid, st)
