@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
                     float a[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float mn = fmaxf(m_ref[h], mx[h]);
+                        // (MOD: a row's reference moves by its own scores only, so that keys of other rows have no effect on it)
+                        const float mn = MOD && !(mx[h] > m_ref[h] + 8.f) ? m_ref[h] : fmaxf(m_ref[h], mx[h]);
                         a[h] = (mn == m_ref[h]) ? 1.f : exp2f(m_ref[h] - mn);
                         m_ref[h] = mn;
                         l_part[h] *= a[h];

@@ -1047,7 +1047,7 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
                           : fixed_ref              ? launch_prefill_cap_tc(p, tk, tv, page_size, static_cast<int>(grid.x),
                                                                            static_cast<int>(n_tiles), st)
-                          : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, fixed_ref, grid, st)
+                          : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, grid, st)
                           : tc                     ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
                           : dtype == KV_DTYPE_BF16 ? launch_prefill_bf16(p, tk, tv, Dh, page_size, grid, st)
                                                    : launch_prefill_f16(p, tk, tv, Dh, page_size, grid, st);

@@ -52,17 +52,17 @@ struct PfCapCfg {
     static constexpr int kOffQ = kRing * kEntry;
     static constexpr int kGroups = 3;            // softmax warpgroups
     static constexpr int kDims = 48;             // dims of O a thread reads out (the last group 32)
-    static constexpr int kOffX = kOffQ + kQB;    // row exchange: [2][kGroups][128] floats, then ints
-    static constexpr int kOffBar = kOffX + 2 * kGroups * 128 * 4 * 2;
-    // full[R], empty[R], s_full[3], p_full[2][3], p_empty[3], q_free, o_full, o_free, done (QK), done (PV), met, next,
-    // tile_full[4], tile_empty[4]
-    static constexpr int kNumBars = 2 * kRing + 12 + 7 + 8;
+    static constexpr int kTileSlots = 4;         // tiles that may be under way
+    static constexpr int kOffX = kOffQ + kQB;    // sums of weights: [tile][first stage][row]
+    static constexpr int kOffBar = kOffX + kTileSlots * kGroups * 128 * 4;
+    // full[R], empty[R], s_full[3], p_full[2][3], p_empty[3], q_free, o_full, o_free, done (QK), done (PV), next,
+    // tile_full[4], tile_empty[4], summed[4]
+    static constexpr int kNumBars = 2 * kRing + 12 + 6 + 3 * kTileSlots;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffDirty = kOffTmem + 8;  // a stage seen in part held a NaN or an infinity in V
     static constexpr int kOffMasks = kOffTmem + 16;
     static constexpr int kOffNext = (kOffMasks + 4 * kMasks + 15) / 16 * 16;  // answer to the request for a tile
-    static constexpr int kTileSlots = 4;         // descriptions of tiles, of 32 words, then the first keys of 128 tokens
-    static constexpr int kTileWords = 32 + 128;
+    static constexpr int kTileWords = 32 + 128;  // a tile's description and the first keys of its up to 128 tokens
     static constexpr int kOffTiles = kOffNext + 16;
     static constexpr int kSmem = 1024 + kOffTiles + kTileSlots * kTileWords * 4;
     static constexpr int kThreads = 128 + 128 * kGroups;
@@ -165,10 +165,10 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t o_full = bars1 + 8;    // every P.V of a tile is done
     const uint32_t o_free = bars1 + 16;   // every softmax warp has read an accumulation out of O
     const uint32_t done_qk = bars1 + 24, done_pv = bars1 + 32;
-    const uint32_t met = bars1 + 40;      // every softmax warp is done with a tile's stages
-    const uint32_t next = bars1 + 48;     // the answer to the request for a tile is there
-    auto tile_full = [&](int i) { return bars1 + 56 + 8u * i; };
-    auto tile_empty = [&](int i) { return bars1 + 56 + 8u * (C::kTileSlots + i); };  // read by the other 15 warps
+    const uint32_t next = bars1 + 40;     // the answer to the request for a tile is there
+    auto tile_full = [&](int i) { return bars1 + 48 + 8u * i; };
+    auto tile_empty = [&](int i) { return bars1 + 48 + 8u * (C::kTileSlots + i); };  // read by the other 15 warps
+    auto summed = [&](int i) { return bars1 + 48 + 8u * (2 * C::kTileSlots + i); };  // by every softmax warp
     // stage numbers below count over the CTA's tiles
     auto kslot = [](int j) { return j % C::kKSlots; };
     auto vslot = [](int j) { return C::kKSlots + j % C::kVSlots; };
@@ -195,11 +195,11 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(o_free, C::kSoftmaxWarps);
         mbar_init(done_qk, 1);
         mbar_init(done_pv, 1);
-        mbar_init(met, C::kSoftmaxWarps);
         mbar_init(next, 1);
         for (int i = 0; i < C::kTileSlots; ++i) {
             mbar_init(tile_full(i), 1);
             mbar_init(tile_empty(i), C::kThreads / 32 - 1);
+            mbar_init(summed(i), C::kSoftmaxWarps);
         }
         *dirty = 0;
         fence_barrier_init();
@@ -458,7 +458,6 @@ __global__ void __launch_bounds__(512, 1)
         const int tr = r / p.g;
         const int od = group * C::kDims;       // first dim this thread reads out
         float* xl = reinterpret_cast<float*>(smem + C::kOffX);
-        int* xok = reinterpret_cast<int*>(smem + C::kOffX) + 2 * kG * 128;
         const CapRowCoef coef = cap_row_coefs(p);
         bool ok = true;
         // warp-uniform outcome: the tensor-memory loads and stores after a wait are warp-collective
@@ -481,29 +480,17 @@ __global__ void __launch_bounds__(512, 1)
         };
 
         int gs = 0, read_out = 0;  // stages of the tiles before this one; tiles read out
-        // the tile that waits for its read-out: its number (-1: none), this thread's row (-1: none), its sum of weights
+        // the tile that waits for its read-out: its number (-1: none), this thread's row (-1: none)
         int last_tile = -1;
         int64_t last_row = -1;
-        float last_l = 0.f;
         // ---- O row / l of the last tile (this thread: dims od .. od + 47)
         auto read_last = [&]() {
-            // all P.V of that tile are done; the tile before was read out, so the parity cannot be an older phase's
-            if (wait(o_full, read_out & 1)) tc_fence_after();
-            const int buf = (read_out & 1) * kG * 128;
+            const int slot = read_out % C::kTileSlots;
+            if (wait(o_full, read_out & 1) && wait(summed(slot), (read_out / C::kTileSlots) & 1)) tc_fence_after();
             ++read_out;
-            xl[buf + group * 128 + r] = last_l;
-            xok[buf + group * 128 + r] = ok ? 1 : 0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(met);
-            wait(met, (read_out - 1) & 1);
             float l = 0.f;
-            bool all = true;
 #pragma unroll
-            for (int k = 0; k < kG; ++k) {
-                l += xl[buf + k * 128 + r];
-                all = all && xok[buf + k * 128 + r] != 0;
-            }
-            ok = __all_sync(0xffffffffu, all && ok);
+            for (int k = 0; k < kG; ++k) l += xl[(slot * kG + k) * 128 + r];
             const bool search = *dirty != 0;
             float* dst = p.out + last_row * DH + od;
             const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -561,7 +548,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int it = 0; read_tile(it, tr, t, row_lo) && t.tile >= 0; ++it) {
             const bool row_valid = tr < t.nt;
             const int64_t row = row_valid ? (int64_t)(t.qs0 + t.t0 + tr) * p.H_q + (int64_t)t.kvh * p.g + r % p.g : -1;
-            if (t.bad_len && t.nt > 0 && t.t0 == 0 && t.kvh == 0 && threadIdx.x == 128) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
+            if (t.nt > 0 && t.bad_len && t.t0 == 0 && t.kvh == 0 && threadIdx.x == 128) raise_err(p.err, KV_DEV_ERR_SEQ_LEN);
             if (t.n_st == 0) {  // no row sees any key
                 if (row_valid)
                     for (int d = od; d < min(DH, od + C::kDims); ++d) p.out[row * DH + d] = 0.f;
@@ -591,7 +578,8 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 release_o();
             };
-            for (int j = (group + 3 - gs % 3) % 3; j < t.n_st && ok; j += 3) {  // stages gs + j of this group
+            const int j0 = (group + 3 - gs % 3) % 3;  // this group's stages: gs + j0, + 3, ...
+            for (int j = j0; j < t.n_st && ok; j += 3) {
                 const int J = gs + j;
                 if (!wait(s_full(J % 3), (J / 3) & 1)) break;
                 while (next_flush <= j && ok) move_o();
@@ -682,7 +670,15 @@ __global__ void __launch_bounds__(512, 1)
             while (ok && next_flush < t.n_st) move_o();
             last_tile = t.tile;
             last_row = row;
-            last_l = l;
+            {
+                // This group's sums of weights, in the order of the tile's stages: which group has the first one depends on the
+                // tiles before, and the total must not. (The slot was read four tiles ago: a stage of this tile is there only after
+                // P.V of the tile three before it, which waited for that read-out.)
+                const int slot = read_out % C::kTileSlots;
+                xl[(slot * kG + j0) * 128 + r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(summed(slot));
+            }
             gs += t.n_st;
         }
         if (last_tile >= 0) read_last();

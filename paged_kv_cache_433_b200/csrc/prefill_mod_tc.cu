@@ -5,15 +5,12 @@
 namespace kvp {
 
 cudaError_t launch_prefill_tc_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int P,
-                                  bool fixed_ref, dim3 grid, cudaStream_t st) {
-    if (dtype == KV_DTYPE_BF16 && fixed_ref)
-        return P == 16 ? launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 16, true>(p, tk, tv, grid, st)
-                       : launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 32, true>(p, tk, tv, grid, st);
+                                  dim3 grid, cudaStream_t st) {
     if (dtype == KV_DTYPE_BF16)
-        return P == 16 ? launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 16, false>(p, tk, tv, grid, st)
-                       : launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 32, false>(p, tk, tv, grid, st);
-    return P == 16 ? launch_prefill_mod_tc_inst<KV_DTYPE_F16, 16, false>(p, tk, tv, grid, st)
-                   : launch_prefill_mod_tc_inst<KV_DTYPE_F16, 32, false>(p, tk, tv, grid, st);
+        return P == 16 ? launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 16>(p, tk, tv, grid, st)
+                       : launch_prefill_mod_tc_inst<KV_DTYPE_BF16, 32>(p, tk, tv, grid, st);
+    return P == 16 ? launch_prefill_mod_tc_inst<KV_DTYPE_F16, 16>(p, tk, tv, grid, st)
+                   : launch_prefill_mod_tc_inst<KV_DTYPE_F16, 32>(p, tk, tv, grid, st);
 }
 
 }  // namespace kvp

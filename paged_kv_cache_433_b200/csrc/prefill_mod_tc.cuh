@@ -14,11 +14,8 @@
 //   - A thread writes P over the S columns that it read itself, so that the two
 //     threads of a row meet only to move the row's reference maximum: they vote
 //     in one barrier whether any row has to, and exchange maxima only then.
-//   - FIXED (bf16, a cap of at most 50, no bias): the cap bounds the scores, one
-//     reference serves every row, and neither maximum nor barrier is needed; the
-//     reference is subtracted by the last multiply-add of the cap's polynomial.
-//     Three softmax warpgroups then work on different stages, one row per
-//     thread in chunks of 32 keys, so that one computes while the others wait.
+//     (prefill_cap_tc.cuh serves bf16 under a cap of at most 50 without a bias:
+//     no reference to move there.)
 //   - hi is rounded, not truncated (pack2_split_near), and O is moved into fp32
 //     sums in registers every kFlushKeys keys: against 64 bits the error is 7e-6
 //     of the result at any length (1.1e-5 at 4096 keys, 7.5e-5 at 32K without).
@@ -43,7 +40,7 @@
 
 namespace kvp {
 
-template <int DH, int P, bool FIXED>
+template <int DH, int P>
 struct PfModCfg {
     static constexpr int kTP = 128;              // keys per stage
     static constexpr int kPPS = kTP / P;         // pages per stage
@@ -56,13 +53,11 @@ struct PfModCfg {
     static constexpr int kRing = kKSlots + kVSlots;
     static constexpr int kQB = 128 * DH * 2;     // Q tile: 128 rows
     static constexpr int kOffQ = kRing * kEntry;
-    // threads per row: each with half of a stage's keys and of the dims; FIXED: each with every third stage and up to
-    // 48 of the dims
-    static constexpr int kParts = FIXED ? 3 : 2;
+    static constexpr int kParts = 2;             // threads per row: each with half of a stage's keys and of the dims
     static constexpr int kOffX = kOffQ + kQB;    // row exchange: [2][kParts][128] floats + ints
     static constexpr int kOffBar = kOffX + 2 * kParts * 128 * 4 * 2;
-    // full[R], empty[R], q_full, s_full[3], p_full[3], p_empty[3], o_full, done (QK), done (PV), o_free
-    static constexpr int kNumBars = 2 * kRing + 1 + 3 + 3 + 3 + 4;
+    // full[R], empty[R], q_full, s_full[3], p_full[3], p_empty[3], o_full, done (QK), done (PV)
+    static constexpr int kNumBars = 2 * kRing + 1 + 3 + 3 + 3 + 3;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
     static constexpr int kOffDirty = kOffTmem + 8;  // a boundary stage held a NaN or an infinity in V
     static constexpr int kSmem = 1024 + kOffTmem + 16;
@@ -72,7 +67,7 @@ struct PfModCfg {
     static constexpr int kFirstSoftmaxWarp = 4;
     // registers per thread after the split: warpgroup 0 (producers, issuers) and the two softmax warpgroups;
     // 128 x kRegsLow + 256 x kRegsHigh must not exceed the launch's 384 x (registers per thread), which the
-    // host checks before the first launch. FIXED: 512 threads of 128 registers, no split.
+    // host checks before the first launch
     static constexpr uint32_t kRegsLow = 64, kRegsHigh = 216;
     static constexpr int kSoftmaxWarps = 4 * kParts;
     static constexpr uint32_t kTmemCols = 512;   // S x 3 (384) + O (128)
@@ -86,11 +81,11 @@ __device__ __forceinline__ uint64_t bits_below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-template <int KT, int DH, int P, bool FIXED>
-__global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
+template <int KT, int DH, int P>
+__global__ void __launch_bounds__(384, 1)
     paged_prefill_mod_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v) {
-    using C = PfModCfg<DH, P, FIXED>;
+    using C = PfModCfg<DH, P>;
     constexpr bool kBF16 = KT == KV_DTYPE_BF16;
     constexpr int kParts = C::kParts;
     constexpr uint32_t kIdescQK = idesc_f16(kBF16, 128, C::kTP, false, false);
@@ -165,7 +160,6 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
     const uint32_t o_full = q_full + 80;
     const uint32_t done_qk = q_full + 88;
     const uint32_t done_pv = q_full + 96;
-    const uint32_t o_free = q_full + 104;  // FIXED: every softmax warp has moved O into its sums
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffTmem);
 
     if (threadIdx.x == 0) {
@@ -175,8 +169,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
         }
         mbar_init(q_full, C::kSoftmaxWarps);
         for (int i = 0; i < 3; ++i) mbar_init(s_full(i), 1);
-        for (int i = 0; i < 3; ++i) mbar_init(p_full(i), FIXED ? 4 : C::kSoftmaxWarps);
-        mbar_init(o_free, C::kSoftmaxWarps);
+        for (int i = 0; i < 3; ++i) mbar_init(p_full(i), C::kSoftmaxWarps);
         for (int i = 0; i < 3; ++i) mbar_init(p_empty(i), 1);
         mbar_init(o_full, 1);
         mbar_init(done_qk, 1);
@@ -199,7 +192,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
     // the register split sits at the top of each warpgroup's branch, so every code path after it is
     // compiled for its own budget
     if (warp < C::kFirstSoftmaxWarp) {
-    if constexpr (!FIXED) regs_dec<C::kRegsLow>();
+    regs_dec<C::kRegsLow>();
     if (warp == 0 || warp == C::kVWarp) {
         // ------------------------------------------------------------ producers
         // warp 0 issues the K boxes of every stage, warp kVWarp the V boxes: two streams of TMA requests
@@ -295,13 +288,11 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
                     const int e = vslot(j);
                     if (!wait(full(e), vphase(j))) break;
                     if (!wait(p_full(j % 3), (j / 3) & 1)) break;
-                    if (FIXED && j > 0 && j % kFlush == 0 && !wait(o_free, (j / kFlush - 1) & 1)) break;
                     tc_fence_after();
                     const uint32_t sV = ring + e * C::kEntry;
                     const uint32_t tP = tmem + (j % 3) * C::kTP;
-                    // each run of 64 keys (FIXED: 32), as one thread writes it over its own S columns: the values, then
-                    // their residuals
-                    constexpr int kRun = FIXED ? 32 : 64;
+                    // each run of 64 keys, as one thread writes it over its own S columns: the values, then their residuals
+                    constexpr int kRun = 64;
                     auto p_col = [](int kk) { return kk * 16 / kRun * kRun + kk * 16 % kRun / 2; };
 #pragma unroll
                     for (int kk = 0; kk < C::kTP / 16; ++kk)
@@ -323,7 +314,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
         __syncwarp();
     }
     } else {
-        if constexpr (!FIXED) regs_inc<C::kRegsHigh>();
+        regs_inc<C::kRegsHigh>();
         // ------------------------------------------------------------ Q tile, softmax, epilogue
         const int quarter = warp & 3;
         const int part = (warp - C::kFirstSoftmaxWarp) >> 2;  // key columns [kH part, + kH) of S, dims of O likewise
@@ -385,8 +376,8 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
             xbuf ^= 1;
         };
         const CapRowCoef coef = cap_row_coefs(p);
-        float m_ref = FIXED ? p.fixed_ref : -INFINITY, l = 0.f;
-        constexpr int kH = FIXED ? 48 : C::kTP / kParts;  // dims of O per thread (and, not FIXED, keys per stage)
+        float m_ref = -INFINITY, l = 0.f;
+        constexpr int kH = C::kTP / kParts;  // keys per stage and dims of O per thread
         const int od = part * kH;                          // first of them
         // earlier accumulations of this thread's part of O, in units of the current reference
         float2 acc[kH / 2];
@@ -395,7 +386,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
         // lanes 0 .. kPPS-1: the page ids of stage j, read one stage ahead; the mask of pages the producers
         // skip (entries outside the pool) is then known without waiting for the V entry
         const int32_t* trow = p.block_tables + (int64_t)b * p.max_blocks + page_first;
-        int pg_cur = !FIXED && lane < C::kPPS && lane < n_pages ? __ldg(trow + lane) : -1;
+        int pg_cur = lane < C::kPPS && lane < n_pages ? __ldg(trow + lane) : -1;
         // A key no row may see (past the tile, or on a page not loaded) may hold stale bytes: zero its V row (this thread:
         // `n` 16-byte chunks of V row r from `chunk` on) once the V entry has landed. In a stage that some rows see only in
         // part a NaN or an infinity in V must not reach the others as 0 times it: those elements are zeroed too, and
@@ -426,7 +417,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
                 }
             }
         };
-        for (int j = 0; !FIXED && j < n_st; ++j) {
+        for (int j = 0; j < n_st; ++j) {
             bool okl = ok;
             const uint32_t tS = tmem + (j % 3) * C::kTP + lane_addr;
             const int nxt = (j + 1) * C::kPPS + lane;
@@ -550,89 +541,6 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full(j % 3));
         }
-        // FIXED: the three softmax warpgroups take every third stage, each its own S buffer, a thread a whole row of 128
-        // keys in four chunks. Nothing passes between them but O: while one waits for its scores the others compute.
-        int next_flush = kFlush;
-        // before stage next_flush, whose P.V starts a new accumulation: this thread's part of O joins its sums
-        auto move_o = [&](bool& okl) {
-            const int jf = next_flush, jp = jf - 1;
-            next_flush += kFlush;
-            // S(jf) is there: P.V(jf - 3) is done, hence P.V(jp - 3), so that the second wait's parity is that of P.V(jp)
-            if (!wait(okl, s_full(jf % 3), (jf / 3) & 1) || !wait(okl, p_empty(jp % 3), (jp / 3) & 1)) return;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < kH / 16; ++q) {
-                if (od + q * 16 >= DH) break;
-                uint32_t a[16];
-                tmem_ld16(tO + lane_addr + od + q * 16, a);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    acc[q * 8 + i] = fadd2(acc[q * 8 + i], make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-        };
-        for (int j = part; FIXED && j < n_st && ok; j += kParts) {
-            if (!wait(ok, s_full(j % 3), (j / 3) & 1)) break;
-            while (next_flush <= j && ok) move_o(ok);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t tS = tmem + (j % 3) * C::kTP + lane_addr;
-            const int kbase = key_first + j * C::kTP;
-            const int np = min(C::kPPS, n_pages - j * C::kPPS);
-            const int pg = lane < np ? __ldg(trow + j * C::kPPS + lane) : -1;
-            const unsigned loaded = __ballot_sync(0xffffffffu, lane < np && pg >= 0 && pg < p.num_pages);
-            const int bad = static_cast<int>(~loaded & ((1u << np) - 1u));
-            const int lim = row_valid ? row_hi - kbase : 0, low = row_lo - kbase;
-            const bool full_stage = lim >= C::kTP && np == C::kPPS && bad == 0 && low <= 0;
-            float2 lsum = make_float2(0.f, 0.f);
-            // (one copy of the chunk's code: unrolled four times it outgrows the instruction caches)
-#pragma unroll 1
-            for (int q = 0; q < C::kTP / 32; ++q) {
-                uint32_t a[32];
-                tmem_ld32(tS + q * 32, a);
-                tmem_wait_ld();
-                float s[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(a[i]);
-                modify_row<true>(p, coef, s, 0.f, 0);
-                if (!full_stage) {
-                    uint32_t see = static_cast<uint32_t>(bits_below(lim - q * 32) & ~bits_below(low - q * 32));
-#pragma unroll
-                    for (int k = 0; k < 32 / P; ++k) {
-                        const int pgi = q * (32 / P) + k;
-                        if (pgi >= np || ((bad >> pgi) & 1)) see &= P == 32 ? 0u : ~(0xffffu << (k * 16));
-                    }
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((see >> c) & 1u)) s[c] = -INFINITY;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p0 = exp2f(s[h * 16 + 2 * i]), p1 = exp2f(s[h * 16 + 2 * i + 1]);
-                        lsum = fadd2(lsum, make_float2(p0, p1));
-                        pack2_split_near<kBF16>(p0, p1, hi[i], lo[i]);
-                    }
-                    tmem_st8(tS + q * 32 + h * 8, hi);
-                    tmem_st8(tS + q * 32 + 16 + h * 8, lo);
-                }
-            }
-            l += lsum.x + lsum.y;
-            tmem_wait_st();
-            clean_v(j, kbase, np, bad, 0, 16, ok);
-            if (!ok) break;
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(j % 3));
-        }
-        while (FIXED && ok && next_flush < n_st) move_o(ok);
-
         // ---- epilogue: O row / l (this thread: dims kH part .. + kH - 1)
         bool okl = ok;
         if (wait(okl, o_full, 0)) tc_fence_after();
@@ -648,7 +556,6 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
             const float inv = l_all != 0.f ? 1.f / l_all : 0.f;
 #pragma unroll
             for (int q = 0; q < kH / 16; ++q) {
-                if (od + q * 16 >= DH) break;
                 uint32_t a[16];
                 tmem_ld16(tO + lane_addr + od + q * 16, a);
                 tmem_wait_ld();
@@ -680,7 +587,7 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
                 __syncwarp();  // the next load is warp-collective
             }
         } else if (row_valid) {
-            for (int d = 0; d < kH && od + d < DH; ++d) dst[d] = 0.f;
+            for (int d = 0; d < kH; ++d) dst[d] = 0.f;
         }
     }
 
@@ -690,11 +597,11 @@ __global__ void __launch_bounds__(FIXED ? 512 : 384, 1)
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int KT, int P, bool FIXED>
+template <int KT, int P>
 cudaError_t launch_prefill_mod_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                                        cudaStream_t st) {
-    using C = PfModCfg<128, P, FIXED>;
-    auto* kern = paged_prefill_mod_tc_kernel<KT, 128, P, FIXED>;
+    using C = PfModCfg<128, P>;
+    auto* kern = paged_prefill_mod_tc_kernel<KT, 128, P>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -708,7 +615,7 @@ cudaError_t launch_prefill_mod_tc_inst(const DecodeParams& p, const CUtensorMap&
         if (e != cudaSuccess) return e;
         const long long pool = static_cast<long long>(fa.numRegs) * C::kThreads;
         const long long need = 128LL * C::kRegsLow + 256LL * C::kRegsHigh;
-        if (!FIXED && need > pool) return cudaErrorInvalidConfiguration;
+        if (need > pool) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);

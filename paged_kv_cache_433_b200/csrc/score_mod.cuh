@@ -107,8 +107,13 @@ __device__ __forceinline__ void cap_scores(const DecodeParams& p, const CapCoef&
 #pragma unroll
         for (int c = 2; c < N; c += 2) big = fmax3_abs(big, x[c], x[c + 1]);
         if (__any_sync(0xffffffffu, big > p.cap_small)) {
+            // which form a score takes goes by itself alone: no other key or row has an effect on it
 #pragma unroll
-            for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c] * p.cap_in) * p.cap_out;
+            for (int c = 0; c < N; c += 2) {
+                const float2 t = cap_small2(k, make_float2(x[c], x[c + 1]));
+                x[c] = fabsf(x[c]) <= p.cap_small ? t.x : tanh_any(x[c] * p.cap_in) * p.cap_out;
+                x[c + 1] = fabsf(x[c + 1]) <= p.cap_small ? t.y : tanh_any(x[c + 1] * p.cap_in) * p.cap_out;
+            }
         } else {
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
@@ -186,27 +191,35 @@ __device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCo
 #pragma unroll
         for (int c = 2; c < N; c += 2) big = fmax3_abs(big, s[c], s[c + 1]);
         auto last = [&](float2 x, float2 r) { return FIXED ? ffma2(x, r, k.neg_ref) : fmul2(x, r); };
+        auto tiny = [&](float2 x) {
+            const float2 z = fmul2(x, x);
+            return last(x, ffma2(z, ffma2(z, k.tiny[2], k.tiny[1]), k.tiny[0]));
+        };
         if (!__any_sync(0xffffffffu, big > p.cap_tiny)) {
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
-                const float2 x = make_float2(s[c], s[c + 1]), z = fmul2(x, x);
-                const float2 t = last(x, ffma2(z, ffma2(z, k.tiny[2], k.tiny[1]), k.tiny[0]));
+                const float2 t = tiny(make_float2(s[c], s[c + 1]));
                 s[c] = t.x;
                 s[c + 1] = t.y;
             }
-        } else if (!__any_sync(0xffffffffu, big > p.cap_small)) {
-#pragma unroll
-            for (int c = 0; c < N; ++c) {  // (scalar: the coefficients come from the constant bank)
-                const float z = s[c] * s[c];
+        } else {
+            // (Scalar: the coefficients come from the constant bank.) Which form a score takes goes by itself alone: no
+            // other key or row has an effect on it.
+            const bool large = __any_sync(0xffffffffu, big > p.cap_small);
+            auto other = [&](float x) {
+                const float z = x * x;
                 float r = p.cap_coef[kCapTerms - 1];
 #pragma unroll
                 for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, p.cap_coef[i]);
-                s[c] = FIXED ? fmaf(s[c], r, k.neg_ref.x) : s[c] * r;
-            }
-        } else {
-            const float ref = FIXED ? p.fixed_ref : 0.f;
+                const float y = FIXED ? fmaf(x, r, k.neg_ref.x) : x * r;
+                return !large || fabsf(x) <= p.cap_small ? y : tanh_any(x * p.cap_in) * p.cap_out - (FIXED ? p.fixed_ref : 0.f);
+            };
 #pragma unroll
-            for (int c = 0; c < N; ++c) s[c] = tanh_any(s[c] * p.cap_in) * p.cap_out - ref;
+            for (int c = 0; c < N; c += 2) {
+                const float2 t = tiny(make_float2(s[c], s[c + 1]));
+                s[c] = fabsf(s[c]) <= p.cap_tiny ? t.x : other(s[c]);
+                s[c + 1] = fabsf(s[c + 1]) <= p.cap_tiny ? t.y : other(s[c + 1]);
+            }
         }
     } else {
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);

@@ -196,3 +196,104 @@ def test_graphs_that_share_a_workspace_and_side_streams():
             run_m()
         side.synchronize()
         assert torch.equal(om, want_m)
+
+
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("mod", [dict(softcap=20.0), dict(softcap=50.0, window=200, docs=True), dict(softcap=3.0, window=1),
+                                 dict(softcap=30.0, prefix=True)], ids=str)
+def test_prefill_mod_capped_many_tiles(mod, P):
+    """Tiles of very different cost, some without rows or visible keys, a chunk longer than its sequence, in a launch that
+    CTAs share out among themselves: eager, on two streams at once, and replayed."""
+    rng = np.random.default_rng(P)
+    B = 48
+    chunks = rng.integers(0, 260, B)
+    chunks[[2, 11]] = 0
+    lens = chunks + (rng.integers(0, 1500, B) * (rng.random(B) < 0.6)).astype(int)
+    lens[20], chunks[20] = 30, 40  # refused
+    c = M._cache(lens, 8, 128, P, "bf16", seed=P)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b) + 9, 16, 128), generator=c["g"], device="cuda").to(torch.bfloat16)
+    ks = None
+    if mod.get("docs"):
+        ks = np.r_[np.maximum(0, pos - rng.integers(0, 300, len(pos))), np.zeros(9, int)]
+        ks[start[5]:start[6]] = 10**6  # a sequence whose rows see nothing
+    prefix = rng.integers(-5, 700, B) if mod.get("prefix") else None
+    cap, win = mod["softcap"], mod.get("window", 0)
+    out = torch.full(q.shape, 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dict(key_start=ks, prefix=prefix, max_q_len=300, softcap=cap, window=win)
+    got = M._prefill(c, q, chunks, 0.09, err=err, out=out, **args)
+    assert int(err) == K.KV_DEV_ERR_SEQ_LEN
+    assert (got[len(b):] == 7).all() and not got[start[20]:start[21]].any()
+    rows = np.unique(np.r_[start[:-1], start[1:] - 1, rng.integers(0, len(b), 60)].clip(0, len(b) - 1))
+    rows = rows[b[rows] != 20]
+    ref, top = M._reference(c, q[torch.from_numpy(rows).cuda()], b[rows], pos[rows], 0.09, cap, None, win,
+                            None if ks is None else ks[rows], prefix)
+    M._close(got[rows], ref, top, str(mod))
+    want = out.clone()
+    d = dict(start=M._d(start), tab=torch.from_numpy(c["tab"]).cuda(), lens=M._d(lens), ks=M._d(ks), pf=M._d(prefix))
+
+    def run(o):
+        K.paged_prefill_attention_mod(o, q, d["start"], 300, c["kp"], c["vp"], d["tab"], d["lens"], 0.09, softcap=cap,
+                                      window=win, key_start=d["ks"], prefix_lens=d["pf"])
+
+    outs, streams = [torch.full(q.shape, 7.0, device="cuda") for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o, s in zip(outs, streams):
+            with torch.cuda.stream(s):
+                run(o)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(outs[0])
+        run(outs[1])
+    for o in outs:
+        o.fill_(7.0)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+@pytest.mark.parametrize("mod", [dict(softcap=20.0), dict(softcap=2.0, alibi=True), dict(window=50), dict()], ids=str)
+@pytest.mark.parametrize("dtype,Dh,kernel", [("bf16", 128, None), ("fp16", 128, None), ("fp16", 64, None),
+                                             ("bf16", 128, K.KV_DECODE_KERNEL_MMA)])
+def test_prefill_mod_hidden_keys_have_no_effect(dtype, Dh, kernel, mod):
+    """Not one bit of a row changes with the keys behind it, in its own tile or in the unused part of a page."""
+    lens, chunks = [301, 90], np.array([150, 90])
+    c = M._cache(lens, 2, Dh, 16, dtype, seed=21)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b), 8, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    mod = dict(mod, alibi_slopes=M._slopes(8)) if mod.get("alibi") else mod
+    mod = {k: v for k, v in mod.items() if k != "alibi"}
+    if kernel is not None:
+        K.paged_decode_set_kernel(kernel)
+    try:
+        first = M._prefill(c, q, chunks, Dh**-0.5, **mod)
+        for s, t0 in ((0, 270), (1, 33)):
+            for t in range(t0, lens[s]):
+                M._put(c, s, t, None, 40.0 if t % 2 else -300.0)
+        for p in ("kp", "vp"):
+            c[p].nan_to_num_(nan=77.0)
+        again = M._prefill(c, q, chunks, Dh**-0.5, **mod)
+    finally:
+        K.paged_decode_set_kernel(K.KV_DECODE_KERNEL_AUTO)
+    same = np.where(b == 0, pos < 270, pos < 33)
+    assert np.array_equal(first[same], again[same]) and not np.array_equal(first, again)
+
+
+@pytest.mark.parametrize("num_splits", [0, 1])
+@pytest.mark.parametrize("mod", [dict(softcap=20.0), dict(softcap=2.0), dict(window=50)], ids=str)
+def test_decode_mod_hidden_keys_have_no_effect(mod, num_splits):
+    lens = [301, 90, 5]
+    c = M._cache(lens, 2, 128, 32, "bf16", seed=22)
+    q = torch.randn((3, 8, 128), generator=c["g"], device="cuda").to(torch.bfloat16)
+    first = M._decode(c, q, 128**-0.5, num_splits, key_start=[3, 44, 2], **mod)
+    for p in ("kp", "vp"):
+        c[p].nan_to_num_(nan=500.0)
+    for s, t1 in ((0, 3), (1, 44), (2, 2)):
+        for t in range(t1):
+            M._put(c, s, t, None, 300.0)
+    assert np.array_equal(first, M._decode(c, q, 128**-0.5, num_splits, key_start=[3, 44, 2], **mod))
