@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(384, 1)
             // this row sees keys [low, lim) of the stage; pages skipped or not loaded are masked
             const int lim = row_valid ? min(C::kTP, row_hi - kbase) : 0;
             const int low = row_lo - kbase;
-            modify_row<false>(p, coef, s, slope, pos - kbase - part * kH);
+            modify_row(p, coef, s, slope, pos - kbase - part * kH);
             if (!(lim == C::kTP && np == C::kPPS && bad == 0 && low <= 0 && okl)) {
                 // this thread's visible columns as bits: from low to lim, on loaded pages
                 constexpr int kPer = kH / P;  // pages among this thread's columns

@@ -166,8 +166,8 @@ __device__ __forceinline__ void modify_cols(const DecodeParams& p, const CapCoef
     }
 }
 
-// The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key. FIXED: minus
-// p.fixed_ref (a cap is set and no bias).
+// The same for one thread's run of N consecutive keys of one row: dist0 = position minus the first key. FIXED (capped
+// chunked prefill: a cap is set and no bias): minus p.fixed_ref.
 struct CapRowCoef {
     float2 tiny[kCapTinyTerms], neg_ref;
 };
@@ -183,43 +183,53 @@ __device__ __forceinline__ CapRowCoef cap_row_coefs(const DecodeParams& p) {
     k.neg_ref = pair(-p.fixed_ref);
     return k;
 }
-template <bool FIXED, int N>
-__device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCoef& k, float (&s)[N], float slope,
-                                           int dist0) {
-    if (FIXED || p.cap_out != 0.f) {
-        float big = fmaxf(fabsf(s[0]), fabsf(s[1]));
+// Largest magnitude of s, for the choices below.
+template <int N>
+__device__ __forceinline__ float largest(const float (&s)[N]) {
+    float big = fmaxf(fabsf(s[0]), fabsf(s[1]));
 #pragma unroll
-        for (int c = 2; c < N; c += 2) big = fmax3_abs(big, s[c], s[c + 1]);
-        auto last = [&](float2 x, float2 r) { return FIXED ? ffma2(x, r, k.neg_ref) : fmul2(x, r); };
-        auto tiny = [&](float2 x) {
-            const float2 z = fmul2(x, x);
-            return last(x, ffma2(z, ffma2(z, k.tiny[2], k.tiny[1]), k.tiny[0]));
-        };
+    for (int c = 2; c < N; c += 2) big = fmax3_abs(big, s[c], s[c + 1]);
+    return big;
+}
+// A pair where both |s| <= p.cap_tiny.
+template <bool FIXED>
+__device__ __forceinline__ float2 cap_tiny2(const CapRowCoef& k, float2 x) {
+    const float2 z = fmul2(x, x);
+    const float2 r = ffma2(z, ffma2(z, k.tiny[2], k.tiny[1]), k.tiny[0]);
+    return FIXED ? ffma2(x, r, k.neg_ref) : fmul2(x, r);
+}
+// Any scores; large: one is above p.cap_small. Which form a score takes goes by itself alone: no other key or row has an
+// effect on it. (Scalar forms: their coefficients come from the constant bank.)
+template <bool FIXED, int N>
+__device__ __forceinline__ void cap_row_any(const DecodeParams& p, const CapRowCoef& k, float (&s)[N], bool large) {
+    auto other = [&](float x) {
+        const float z = x * x;
+        float r = p.cap_coef[kCapTerms - 1];
+#pragma unroll
+        for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, p.cap_coef[i]);
+        const float y = FIXED ? fmaf(x, r, k.neg_ref.x) : x * r;
+        return !large || fabsf(x) <= p.cap_small ? y : tanh_any(x * p.cap_in) * p.cap_out - (FIXED ? p.fixed_ref : 0.f);
+    };
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 t = cap_tiny2<FIXED>(k, make_float2(s[c], s[c + 1]));
+        s[c] = fabsf(s[c]) <= p.cap_tiny ? t.x : other(s[c]);
+        s[c + 1] = fabsf(s[c + 1]) <= p.cap_tiny ? t.y : other(s[c + 1]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCoef& k, float (&s)[N], float slope, int dist0) {
+    if (p.cap_out != 0.f) {
+        const float big = largest(s);
         if (!__any_sync(0xffffffffu, big > p.cap_tiny)) {
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
-                const float2 t = tiny(make_float2(s[c], s[c + 1]));
+                const float2 t = cap_tiny2<false>(k, make_float2(s[c], s[c + 1]));
                 s[c] = t.x;
                 s[c + 1] = t.y;
             }
         } else {
-            // (Scalar: the coefficients come from the constant bank.) Which form a score takes goes by itself alone: no
-            // other key or row has an effect on it.
-            const bool large = __any_sync(0xffffffffu, big > p.cap_small);
-            auto other = [&](float x) {
-                const float z = x * x;
-                float r = p.cap_coef[kCapTerms - 1];
-#pragma unroll
-                for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, p.cap_coef[i]);
-                const float y = FIXED ? fmaf(x, r, k.neg_ref.x) : x * r;
-                return !large || fabsf(x) <= p.cap_small ? y : tanh_any(x * p.cap_in) * p.cap_out - (FIXED ? p.fixed_ref : 0.f);
-            };
-#pragma unroll
-            for (int c = 0; c < N; c += 2) {
-                const float2 t = tiny(make_float2(s[c], s[c + 1]));
-                s[c] = fabsf(s[c]) <= p.cap_tiny ? t.x : other(s[c]);
-                s[c + 1] = fabsf(s[c + 1]) <= p.cap_tiny ? t.y : other(s[c + 1]);
-            }
+            cap_row_any<false>(p, k, s, __any_sync(0xffffffffu, big > p.cap_small));
         }
     } else {
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
@@ -230,7 +240,6 @@ __device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCo
             s[c + 1] = t.y;
         }
     }
-    if (FIXED) return;
     if (p.alibi_slopes != nullptr) {
         const float d = static_cast<float>(dist0);
 #pragma unroll
