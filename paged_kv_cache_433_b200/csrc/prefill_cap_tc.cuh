@@ -518,22 +518,23 @@ __global__ void __launch_bounds__(512, 1)
                     bool again = search;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) again = again || o[i] != o[i];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(dst + q * 16 + i) =
+                            make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
                     if (again && l == l && ok) {
                         const int rest = last_tile / tiles_x, b = rest / p.H_kv, kvh = rest % p.H_kv;
                         const int qs0 = p.q_start[b], i0 = last_tile % tiles_x * p.q_tile + tr, len = p.seq_lens[b];
                         const int pos = len - (p.q_start[b + 1] - qs0) + i0;
                         const int lo = first_key(p, qs0 + i0, pos);
                         const int hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0);
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<true>(p, b, kvh, P, DH, od + q * 16 + i, lo, hi);
-                            o[i] = o[i] != o[i] ? x : o[i] + x;
+                            const float x = sum_nonfinite<true>(p, b, kvh, P, DH, od + q * 16 + i, lo, hi) * inv;
+                            float& y = dst[q * 16 + i];
+                            y = y != y ? x : y + x;
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4*>(dst + q * 16 + i) =
-                            make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
                 }
                 __syncwarp();  // the next load is warp-collective
             }
@@ -673,6 +674,7 @@ __global__ void __launch_bounds__(512, 1)
                     // S(J) is there, so P.V(J - 3) is done and read the entry's fill before: the parity is this fill's
                     if (!wait(full(vslot(J)), vphase(J))) break;
                     const uint32_t at0 = ring + vslot(J) * C::kEntry + r * 128;
+#pragma unroll 1
                     for (int c = 0; c < DH / 8; ++c) {
                         const uint32_t at = at0 + (c >> 3) * C::kBoxB + (c & 7) * 16;
                         if (stale) {

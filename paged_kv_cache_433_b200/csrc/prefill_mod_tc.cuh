@@ -572,17 +572,18 @@ __global__ void __launch_bounds__(384, 1)
                     bool again = dirty;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) again = again || o[i] != o[i];
-                    if (again && l_all == l_all) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi);
-                            o[i] = o[i] != o[i] ? x : o[i] + x;
-                        }
-                    }
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4*>(dst + q * 16 + i) =
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                    if (again && l_all == l_all) {
+#pragma unroll 1
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi) * inv;
+                            float& y = dst[q * 16 + i];
+                            y = y != y ? x : y + x;
+                        }
+                    }
                 }
                 __syncwarp();  // the next load is warp-collective
             }
