@@ -252,7 +252,8 @@ int kv_rope_append(void* k_pages, void* v_pages, void* q_out, const void* q, con
  * q and q_out both NULL: no queries), the k and v rows at slot_mapping[b]
  * (-1 skips the cache write; a slot past the pool sets KV_DEV_ERR_SLOT), and,
  * when k_out is not NULL, the k rows to k_out (contiguous [B][H_kv][Dh]) --
- * for a cache that is written by a quantising append. k_pages, v_pages, v_new
+ * for a cache that is written by a quantising append. The slots of a call must
+ * be distinct. k_pages, v_pages, v_new
  * and slot_mapping may be NULL together when k_out is set.
  *   q_stride, k_stride, v_stride: elements from one token's rows to the next
  *   (heads of a token are contiguous), so that q, k_new and v_new may be slices
@@ -423,7 +424,8 @@ int paged_decode_attention_fp8(float* out, const void* q, int32_t q_dtype, const
  * an infinity gets scale NaN and reads back as NaN. k_new, v_new of src_dtype
  * (bf16, fp16 or fp32), tokens k_stride / v_stride elements apart (heads
  * contiguous; at least H_kv * Dh, a multiple of 16 bytes). Dh / 16 must be a
- * power of two up to 32 (else KV_ERR_UNSUPPORTED). Slots as kv_append. */
+ * power of two up to 32 (else KV_ERR_UNSUPPORTED). Slots as kv_append; those of
+ * a call must be distinct (two tokens' codes and scales could mix). */
 int kv_append_int8(void* k_pages, void* v_pages, float* kv_scales, const void* k_new, const void* v_new,
                    int64_t k_stride, int64_t v_stride, int32_t src_dtype, const int64_t* slot_mapping, int32_t B,
                    int32_t H_kv, int32_t Dh, int32_t page_size, int32_t num_pages, int* err_flag, void* stream);
@@ -454,11 +456,13 @@ int kv_copy_pages_int8(void* k_pages, void* v_pages, float* kv_scales, const int
  * {64, 128}, page_size in {16, 32}, num_pages * H_kv * page_size < 2^31);
  * errors as paged_decode_attention. num_splits > 0: that many ranges per row,
  * merged by a second kernel; 0: persistent CTAs that share the batch's pages
- * equally (B <= 1024; a split by the host's rule above), rows cut between them
- * merged by a second kernel; no second kernel where no row can be longer than
- * 256 tokens. workspace: paged_decode_ext_workspace_bytes. A block-table entry
- * outside the pool skips that page only. NaN scales of visible tokens give NaN rows; codes and scales
- * behind a sequence's length are never used. */
+ * equally (B <= 1024; above, a split by the host's rule), rows cut between them
+ * merged by a second kernel; ranges of 128 tokens where one wave of CTAs holds
+ * them all, and no second kernel where no row can be longer than 256 tokens.
+ * workspace: paged_decode_ext_workspace_bytes; not shared by calls that may run
+ * at the same time. A block-table entry outside the pool skips that page only.
+ * NaN scales of visible tokens give NaN rows; codes and scales behind a
+ * sequence's length are never used. */
 int paged_decode_attention_int8(float* out, const void* q, int32_t q_dtype, const void* k_pages, const void* v_pages,
                                 const float* kv_scales, const int32_t* block_tables, int32_t max_blocks,
                                 const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh,
@@ -487,8 +491,9 @@ int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32
  * device int32 [B]: tokens that every row of the sequence's chunk sees, before
  * or behind its own position (prefill). A row with lo >= hi gets zeros. Keys
  * that a row does not see have no effect on it, whatever they hold (NaN and
- * infinities in K and V included); a NaN among the scores or values it sees
- * gives NaN, an infinity among the values its sign. Pages before the first visible key are not read (their table
+ * infinities in K and V included: not a bit of the row depends on them); a NaN
+ * among the scores or values it sees gives NaN, an infinity among the values
+ * its sign. Pages before the first visible key are not read (their table
  * entries may be anything).
  * softcap: 0 (none) or positive and finite; window: 0 (none) or positive.
  * bf16 / fp16 K/V, H_q / H_kv <= 64, Dh in {64, 128}, page_size in {16, 32},
@@ -507,8 +512,9 @@ int paged_decode_attention_mod(float* out, const void* q, const void* k_pages, c
 
 /* Chunk form: rows, q_start, max_q_len and errors as paged_prefill_attention
  * (a bidirectional prefix may reach behind the chunk's rows, never behind
- * seq_lens[b]). The tcgen05 kernel for Dh = 128 and groups that divide 128
- * under AUTO and TCGEN05, the warp-MMA kernel otherwise. */
+ * seq_lens[b]). tcgen05 kernels for Dh = 128 and groups that divide 128 under
+ * AUTO and TCGEN05 (one of its own for bf16 under a cap of at most 50 without
+ * slopes), the warp-MMA kernel otherwise. Results repeat bit for bit. */
 int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
                                 const void* k_pages, const void* v_pages, const int32_t* block_tables,
                                 int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,

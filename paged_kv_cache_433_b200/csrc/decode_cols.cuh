@@ -21,7 +21,7 @@
 // probabilities.
 //
 // Probabilities go into the second product as a 16-bit value plus its rounded
-// residual. Their fragment (token rows, head columns) becomes the second
+// residual (bf16 K/V: and that one's). Their fragment (token rows, head columns) becomes the second
 // product's B operand by movmatrix, 8 x 8 at a time. With at most 4 heads
 // (DUP), columns 4..7 repeat the queries of columns 0..3: their lanes compute
 // the same probabilities and hand over the residuals, so one MMA does both.
@@ -184,6 +184,10 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
     constexpr bool kQBF16 = KT == KV_DTYPE_BF16;         // QK operands of 16-bit K/V: bf16, else f16
     constexpr bool kPBF16 = kI8 || KT == KV_DTYPE_BF16;   // PV operands (int8: bf16, whose range holds any V scale)
     constexpr int kTP = C::kTP, kKS = DH / 16, kMT = kTP / 16, kOM = DH / 16, kUPS = C::kUPS;
+    // 16-bit bf16 K/V: a third term of the probabilities, so that they keep 24 bits (2.3e-7 of the result off; 2.4e-6 with
+    // two, in the same 69 us: the product waits for memory). int8, bound by its instructions, keeps two (61.5 us; 65.3 with
+    // three): its values are rounded to 8 bits anyway. fp16 has 22 bits with two.
+    constexpr bool kThird = MOD && kPBF16;
     static_assert(!DUP || NT == 1, "doubled columns");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
 
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
             }
 
             // ---- probabilities, transposed into the B operand (tokens 2 quad, + 1 of each block of 8; head lane / 4)
-            uint32_t ph[NT][kMT][2], pl[NT][kMT][2];
+            uint32_t ph[NT][kMT][2], pl[NT][kMT][2], pr[NT][kMT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -606,6 +610,12 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                             ph[nt][mt][h] = movmatrix_trans(hi);
                             pl[nt][mt][h] = movmatrix_trans(lo);
                         }
+                        if constexpr (kThird) {
+                            const uint32_t rest = pack2<true>(pv[0] - __uint_as_float(hi << 16) - __uint_as_float(lo << 16),
+                                                              pv[1] - __uint_as_float(hi & 0xffff0000u) -
+                                                                  __uint_as_float(lo & 0xffff0000u));
+                            pr[nt][mt][h] = movmatrix_trans(DUP && quad >= 2 ? 0u : rest);
+                        }
                     }
 
             // ---- V rows that no head sees may hold NaN (int8 codes cannot): zero them
@@ -624,10 +634,12 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
 
             // ---- O^T += V^T P^T: sixteen tokens a product, added to fp32 sums. (Sums kept in the MMA's accumulator,
             // which rounds towards zero, cost the same time and grow less exact with the length: score_mod.cuh.)
-            auto add_pv = [&](float(&sum)[4], const uint32_t(&a)[4], const uint32_t(&hi)[2], const uint32_t(&lo)[2]) {
+            auto add_pv = [&](float(&sum)[4], const uint32_t(&a)[4], const uint32_t(&hi)[2], const uint32_t(&lo)[2],
+                              const uint32_t(&rest)[2]) {
                 float d[4] = {};
-                mma_16816<kPBF16>(d, a, hi[0], hi[1]);
+                if constexpr (kThird) mma_16816<true>(d, a, rest[0], rest[1]);
                 if constexpr (!DUP) mma_16816<kPBF16>(d, a, lo[0], lo[1]);
+                mma_16816<kPBF16>(d, a, hi[0], hi[1]);
                 const float2 x = fadd2(make_float2(sum[0], sum[1]), make_float2(d[0], d[1]));
                 const float2 y = fadd2(make_float2(sum[2], sum[3]), make_float2(d[2], d[3]));
                 sum[0] = x.x, sum[1] = x.y, sum[2] = y.x, sum[3] = y.y;
@@ -660,7 +672,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                             s8x4_to_bf16x2x2(byte_perm(wv[2][m], wv[3][m], sel), a[2], a[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                add_pv(o[nt][2 * m + hh], a, ph[nt][ks], pl[nt][ks]);
+                                add_pv(o[nt][2 * m + hh], a, ph[nt][ks], pl[nt][ks], pr[nt][ks]);
                         }
                 } else {
 #pragma unroll
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         uint32_t a[4];
                         ldsm_x4_trans(sV + (c >> 3) * C::kBoxB + swz<128>(t, c), a[0], a[1], a[2], a[3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) add_pv(o[nt][m], a, ph[nt][ks], pl[nt][ks]);
+                        for (int nt = 0; nt < NT; ++nt) add_pv(o[nt][m], a, ph[nt][ks], pl[nt][ks], pr[nt][ks]);
                     }
                 }
             }

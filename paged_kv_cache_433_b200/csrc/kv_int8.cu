@@ -59,8 +59,9 @@ __device__ __forceinline__ uint4 quantise16(const float (&x)[16], int32_t cpr, u
 }
 
 // One thread takes the same sixteen elements of a token's K and V row (one 16-byte vector of codes each): four loads in
-// flight, issued beside that of the slot. Bound by memory: 8185 tokens of 8 heads 15.4 us with a thread per K or V
-// vector, the slot read first.
+// flight, issued beside that of the slot. Bound by memory: 8185 tokens of 8 heads of 128 (bf16) take 14.7 us, 3.4 TB/s (0.52
+// of the measured copy rate, at a size where a launch's start and end weigh as much as its middle); 15.4 us with a thread
+// per K or V vector and the slot read first.
 template <int DT>
 __global__ void __launch_bounds__(256) kv_append_int8_kernel(uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
                                                              float* __restrict__ scales, const uint4* __restrict__ k_new,
@@ -115,7 +116,8 @@ __device__ __forceinline__ void widen16(const uint4& v, float s, uint4* dst) {
 // blockIdx.x: page pair; the units (16 codes) of that page's K and V codes run
 // over the threads of the blockIdx.y CTAs, four to a thread with their loads
 // issued together. Bound by memory (one read of the codes, one write of the
-// values).
+// values): the pages of 8185 tokens of 8 heads of 128 to bf16 in 13.3 us, 3.8
+// TB/s.
 template <int DT>
 __global__ void __launch_bounds__(256) kv_dequant_pages_int8_kernel(
     uint4* __restrict__ k_out, uint4* __restrict__ v_out, const uint4* __restrict__ k_pages,

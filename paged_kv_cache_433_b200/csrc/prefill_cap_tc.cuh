@@ -14,10 +14,16 @@
 //
 // The grid has a CTA per tile, but a CTA that is done with its tile takes the place of one that has not started
 // (clusterlaunchcontrol) and goes on, so that in effect one CTA per SM walks through tiles (whose costs differ: handed out
-// in a fixed order the same work took 27 % longer). Stages, barriers and ring entries are counted over all of its tiles.
-// Warp 0 asks for the next tile and lays its description out for the other warps; loads and Q K^T run ahead into it, and a
-// warpgroup computes its first stage of it before it reads out O of the last one, for which it has to wait for the slowest.
-// A tile's start and end, about 10 us with a CTA each, are hidden that way -- windowed layers have few stages per tile.
+// in a fixed order the windowed case below took 345 us instead of 310). Stages, barriers and ring entries are counted over
+// all of its tiles. Warp 0 asks for the next tile and lays its description out for the other warps; loads and Q K^T run
+// ahead into it, and a warpgroup computes its first stage of it before it reads out O of the last one, for which it has to
+// wait for the slowest. A tile's start and end, about 10 us with a CTA each, are hidden that way -- windowed layers have few stages per tile.
+//
+// Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 435 us, 672 TFLOP/s counted once, 1008 with the
+// residuals' products (a CTA per tile: 475 us; without the cap, prefill_tc.cuh: 425-430). Two prompts of 4096 tokens in
+// documents of 1500 under a window of 1024, cap 30: 300 us (a CTA per tile: 340). Bound by the chain Q K^T -> softmax ->
+// P V of a stage, about 10,400 cycles at three stages in flight: the matrix pipe is busy for 1,536 cycles a stage, the
+// exponentials for 1,024, and tensor memory has no room for a fourth buffer of scores.
 //
 // O is moved into fp32 sums in registers every kFlushKeys keys (score_mod.cuh). V rows that no row of the tile sees are
 // zeroed, and in a stage that some rows see only in part NaN and infinities too; the rows that do see them add them from
