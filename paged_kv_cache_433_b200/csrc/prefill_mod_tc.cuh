@@ -16,8 +16,8 @@
 //     in one barrier whether any row has to, and exchange maxima only then.
 //     (prefill_cap_tc.cuh serves bf16 under a cap of at most 50 without a bias:
 //     no reference to move there.)
-//   - hi is rounded, not truncated (pack2_split_near), and O is moved into fp32
-//     sums in registers every kFlushKeys keys: against 64 bits the error is 7e-6
+//   - value and residual are rounded, not truncated (pack2_split_near), and O is moved into fp32
+//     sums in registers every kFlushKeys keys: against 64 bits the error is 5e-6
 //     of the result at any length (1.1e-5 at 4096 keys, 7.5e-5 at 32K without).
 //   - A stage that some rows see only in part ("boundary") has its V rows
 //     searched for NaN and infinity, which a probability of 0 would not keep

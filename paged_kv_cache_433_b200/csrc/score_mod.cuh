@@ -252,7 +252,7 @@ __device__ __forceinline__ void modify_row(const DecodeParams& p, const CapRowCo
 // tcgen05 alike), and up to n / 8 times 2^-23 for values of one sign (1.0e-5 at 2048). The multi-token kernels
 // therefore move their output accumulators into fp32 sums after every kFlushKeys keys, in registers (tcgen05) or in the
 // output rows that the same threads write at the end (warp MMA). More often costs more than it gives: 8 chunks of 512
-// tokens over 4096, capped, 435 us at 2048 keys and 6.8e-6 off; 464 us at 1024 and 5.5e-6; 520 us at 512 and 5.1e-6
+// tokens over 4096, capped, 435 us at 2048 keys and 5.3e-6 off; 464 us at 1024; 520 us at 512
 // (the rest is the 16-bit splitting of the probabilities).
 constexpr int kFlushKeys = 2048;
 

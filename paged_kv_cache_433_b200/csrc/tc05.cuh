@@ -59,16 +59,15 @@ __device__ __forceinline__ void pack2_split_fast(float x0, float x1, uint32_t& h
     }
 }
 
-// As pack2_split_fast with hi rounded to nearest for bf16 (one packed conversion in place of a byte permute): the
-// residual takes either sign, so truncating it leaves errors of at most 2^-16 without a common sign, where both
-// truncated make every probability too small by 2^-17 on average (a sum over thousands of keys: 1.2e-5 against
-// 2e-6 of the result).
+// As pack2_split_fast with both rounded to nearest for bf16 (packed conversions in place of byte permutes, at the same
+// time): errors of at most 2^-18 without a common sign, where both truncated make every probability too small by 2^-17 on
+// average (a sum over thousands of keys: 1.2e-5 of the result).
 template <bool IS_BF16>
 __device__ __forceinline__ void pack2_split_near(float x0, float x1, uint32_t& hi, uint32_t& lo) {
     if constexpr (IS_BF16) {
         hi = pack2<true>(x0, x1);
         const float2 r = fsub2(make_float2(x0, x1), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
-        lo = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
+        lo = pack2<true>(r.x, r.y);
     } else {
         pack2_split<false>(x0, x1, hi, lo);
     }
