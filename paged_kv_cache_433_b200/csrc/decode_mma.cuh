@@ -178,11 +178,16 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     if constexpr (QM) {
         split = 0;
         kvh = blockIdx.y;
-        b = blockIdx.z;
         chunk_pages = 0;
-        qs0 = p.q_start[b];
-        n_q = p.q_start[b + 1] - qs0;
-        t0 = blockIdx.x * p.q_tile;
+        if constexpr (MOD) {
+            const ChunkTile ct = chunk_tile(p, blockIdx.x, threadIdx.x & 31);
+            b = ct.b, qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
+        } else {
+            b = blockIdx.z;
+            qs0 = p.q_start[b];
+            n_q = p.q_start[b + 1] - qs0;
+            t0 = blockIdx.x * p.q_tile;
+        }
         if (t0 >= n_q) return;
         nt = min(p.q_tile, n_q - t0);
     } else if (p.items != nullptr) {

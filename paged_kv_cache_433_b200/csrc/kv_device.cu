@@ -968,6 +968,7 @@ namespace {
 
 // mod: the modified scores and masks of paged_prefill_attention_mod (nullptr: plain causal attention).
 struct PrefillMod {
+    int32_t n_rows;
     float softcap;
     const float* alibi_slopes;
     int32_t window;
@@ -985,7 +986,8 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     const int32_t g = H_q / H_kv;
     if (g > 64) return KV_ERR_UNSUPPORTED;
     if (B < 0 || max_q_len < 0 || max_blocks <= 0 || num_pages <= 0) return KV_ERR_ARG;
-    if (B == 0 || max_q_len == 0) return KV_OK;
+    if (mod && mod->n_rows < 0) return KV_ERR_ARG;
+    if (B == 0 || max_q_len == 0 || (mod && mod->n_rows == 0)) return KV_OK;
     if (B > 65535 || H_kv > 65535) return KV_ERR_UNSUPPORTED;
     if (!out || !q || !q_start || !k_pages || !v_pages || !block_tables || !seq_lens) return KV_ERR_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages)) return KV_ERR_ARG;
@@ -1001,7 +1003,7 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
         const int sms = sm_count();
         if (sms <= 0) return KV_ERR_CUDA;
         const int32_t small = std::max(1, 16 / g);
-        const int64_t tiles = (static_cast<int64_t>(max_q_len) + small - 1) / small * H_kv * B;
+        const int64_t tiles = (static_cast<int64_t>(mod->n_rows) / small + B) * H_kv;
         if (tiles <= 2 * sms && static_cast<int64_t>(max_blocks) * page_size <= 2LL * kFlushKeys) q_tile = small;
     }
     DecodeParams p{};
@@ -1039,9 +1041,10 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;
     if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) || !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
         return KV_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>((max_q_len + q_tile - 1) / q_tile), static_cast<unsigned>(H_kv),
-                    static_cast<unsigned>(B));
-    const int64_t n_tiles = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+    // mod: the tiles of all sequences behind one another (chunk_tile in score_mod.cuh)
+    const dim3 grid(static_cast<unsigned>(mod ? mod->n_rows / q_tile + B : (max_q_len + q_tile - 1) / q_tile),
+                    static_cast<unsigned>(H_kv), static_cast<unsigned>(mod ? 1 : B));
+    const int64_t n_tiles = static_cast<int64_t>(grid.x) * grid.y;
     fixed_ref = fixed_ref && tc && n_tiles < (1LL << 31);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
@@ -1068,7 +1071,7 @@ int paged_prefill_attention(float* out, const void* q, const int32_t* q_start, i
                         Dh, page_size, num_pages, scale, dtype, err_flag, stream, nullptr);
 }
 
-int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len,
+int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len, int32_t n_rows,
                                 const void* k_pages, const void* v_pages, const int32_t* block_tables,
                                 int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
                                 int32_t Dh, int32_t page_size, int32_t num_pages, float scale, int32_t dtype,
@@ -1076,7 +1079,7 @@ int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_star
                                 const int32_t* prefix_lens, int* err_flag, void* stream) {
     const int rc = check_mod(softcap, window);
     if (rc != KV_OK) return rc;
-    const PrefillMod mod{softcap, alibi_slopes, window, key_start, prefix_lens};
+    const PrefillMod mod{n_rows, softcap, alibi_slopes, window, key_start, prefix_lens};
     return prefill_impl(out, q, q_start, max_q_len, k_pages, v_pages, block_tables, max_blocks, seq_lens, B, H_q, H_kv,
                         Dh, page_size, num_pages, scale, dtype, err_flag, stream, &mod);
 }

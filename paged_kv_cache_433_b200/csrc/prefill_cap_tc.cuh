@@ -87,16 +87,16 @@ struct CapTile {
 };
 static_assert(sizeof(CapTile) <= 32 * 4, "description of a tile");
 template <int P>
-__device__ __forceinline__ CapTile cap_tile(const DecodeParams& p, int tile, int tiles_x, int lane) {
+__device__ __forceinline__ CapTile cap_tile(const DecodeParams& p, int tile, int slots, int lane) {
     constexpr int kTP = PfCapCfg<P>::kTP;
     CapTile t;
     t.tile = tile;
-    const int x = tile % tiles_x, rest = tile / tiles_x;
-    t.kvh = rest % p.H_kv;
-    t.b = rest / p.H_kv;
-    t.qs0 = p.q_start[t.b];
-    const int n_q = p.q_start[t.b + 1] - t.qs0, len = p.seq_lens[t.b];
-    t.t0 = x * p.q_tile;
+    const ChunkTile ct = chunk_tile(p, tile % slots, lane);
+    t.kvh = tile / slots;
+    t.b = ct.b;
+    t.qs0 = ct.qs0;
+    const int n_q = ct.n_q, len = p.seq_lens[t.b];
+    t.t0 = ct.t0;
     t.nt = min(p.q_tile, n_q - t.t0);
     t.bad_len = len < 0 || len > p.max_blocks * P || n_q > len;
     t.pos0 = len - n_q + t.t0;
@@ -142,7 +142,7 @@ __device__ __forceinline__ uint32_t bits32_below(int n) { return n <= 0 ? 0u : n
 template <int P>
 __global__ void __launch_bounds__(512, 1)
     paged_prefill_cap_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
-                                const __grid_constant__ CUtensorMap tmap_v, const int tiles_x) {
+                                const __grid_constant__ CUtensorMap tmap_v, const int slots) {
     using C = PfCapCfg<P>;
     constexpr int DH = C::kDH, kTP = C::kTP, kG = C::kGroups;
     constexpr uint32_t kIdescQK = idesc_f16(true, 128, kTP, false, false);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(512, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 int* d = reinterpret_cast<int*>(smem + C::kOffTiles) + slot * C::kTileWords;
-                if (tile >= 0) t = cap_tile<P>(p, tile, tiles_x, lane);
+                if (tile >= 0) t = cap_tile<P>(p, tile, slots, lane);
                 t.tile = tile;
                 if (lane == 0) *reinterpret_cast<CapTile*>(d) = t;
                 for (int i = lane; tile >= 0 && !t.bad_len && i < t.nt; i += 32)
@@ -529,10 +529,10 @@ __global__ void __launch_bounds__(512, 1)
                         *reinterpret_cast<float4*>(dst + q * 16 + i) =
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
                     if (again && l == l && ok) {
-                        const int rest = last_tile / tiles_x, b = rest / p.H_kv, kvh = rest % p.H_kv;
-                        const int qs0 = p.q_start[b], i0 = last_tile % tiles_x * p.q_tile + tr, len = p.seq_lens[b];
-                        const int pos = len - (p.q_start[b + 1] - qs0) + i0;
-                        const int lo = first_key(p, qs0 + i0, pos);
+                        const ChunkTile ct = chunk_tile(p, last_tile % slots);
+                        const int b = ct.b, kvh = last_tile / slots, i0 = ct.t0 + tr, len = p.seq_lens[b];
+                        const int pos = len - ct.n_q + i0;
+                        const int lo = first_key(p, ct.qs0 + i0, pos);
                         const int hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0);
 #pragma unroll 1
                         for (int i = 0; i < 16; ++i) {
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 template <int P>
-cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles_x,
+cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int slots,
                                        int n_tiles, cudaStream_t st) {
     using C = PfCapCfg<P>;
     auto* kern = paged_prefill_cap_tc_kernel<P>;
@@ -741,7 +741,7 @@ cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap&
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_pdl(kern, dim3(static_cast<unsigned>(n_tiles)), dim3(C::kThreads), C::kSmem, st, p, tk, tv, tiles_x);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(n_tiles)), dim3(C::kThreads), C::kSmem, st, p, tk, tv, slots);
 }
 
 }  // namespace kvp

@@ -103,11 +103,10 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0) grid_launch_dependents();
 
     // ---- this CTA's tile: chunk tokens t0 .. t0 + nt - 1 of sequence b, KV head kvh
-    const int kvh = blockIdx.y, b = blockIdx.z;
+    const ChunkTile ct = chunk_tile(p, blockIdx.x, lane);
+    const int kvh = blockIdx.y, b = ct.b;
     const int g = p.g;
-    const int qs0 = p.q_start[b];
-    const int n_q = p.q_start[b + 1] - qs0;
-    const int t0 = blockIdx.x * p.q_tile;
+    const int qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
     if (t0 >= n_q) return;
     const int nt = min(p.q_tile, n_q - t0);
     int len = p.seq_lens[b];

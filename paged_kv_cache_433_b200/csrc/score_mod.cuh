@@ -22,6 +22,45 @@ __device__ __forceinline__ int first_key(const DecodeParams& p, int row, int pos
     return first_visible_key(pos, p.window, p.key_start, row);
 }
 
+// The grids of the chunked prefill with modified scores: sequence b has the tile slots from q_start[b] / q_tile + b on, as
+// many as its rows can need, n_rows / q_tile + B in all whatever the chunks' lengths are. (A slot per sequence and tile of
+// the longest chunk, with one chunk of 4096 among 256: 262144 tiles, 1.8 ms for nothing.) Slots past a chunk's end have
+// t0 >= n_q.
+struct ChunkTile {
+    int b, qs0, n_q, t0;  // sequence, its first row, its rows; the tile's first row of them
+};
+__device__ __forceinline__ int first_slot(const DecodeParams& p, int b) { return p.q_start[b] / p.q_tile + b; }
+__device__ __forceinline__ ChunkTile tile_of(const DecodeParams& p, int b, int slot) {
+    ChunkTile t;
+    t.b = b;
+    t.qs0 = p.q_start[b];
+    t.n_q = p.q_start[b + 1] - t.qs0;
+    t.t0 = (slot - first_slot(p, b)) * p.q_tile;
+    if (t.t0 < 0) t.n_q = t.t0 = 0;  // (a first row other than 0)
+    return t;
+}
+// The tile in `slot`; called by whole warps: the last sequence whose slots begin no later, 32 candidates a step.
+__device__ __forceinline__ ChunkTile chunk_tile(const DecodeParams& p, int slot, int lane) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, c = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, lane == 0 || (c < hi && first_slot(p, c) <= slot));
+        lo += (31 - __clz(m)) * step;
+        hi = min(hi, lo + step);
+    }
+    return tile_of(p, lo, slot);
+}
+// The same for one thread.
+__device__ __forceinline__ ChunkTile chunk_tile(const DecodeParams& p, int slot) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_slot(p, mid) <= slot) lo = mid;
+        else hi = mid;
+    }
+    return tile_of(p, lo, slot);
+}
+
 // Keys of a tile of nt query rows (chunk tokens) at positions pos0 ..: some row sees keys in [begin, end) only;
 // every row sees all keys in [all0, all1). Called by whole warps.
 struct TileKeys {

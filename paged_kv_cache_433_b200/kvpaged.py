@@ -101,7 +101,7 @@ SIGNATURES = [
       _vp, _sz, _vp, _vp]),
     ("paged_decode_ext_workspace_bytes", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _psz]),
     ("paged_prefill_attention_mod", ctypes.c_int,
-     [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32,
+     [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _f32, _vp, _i32,
       _vp, _vp, _vp, _vp]),
     ("paged_decode_set_kernel", ctypes.c_int, [_i32]),
     ("paged_decode_num_splits", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _pi32]),
@@ -726,8 +726,8 @@ def paged_prefill_attention_mod(out, q, q_start, max_q_len: int, k_pages, v_page
     B, mb, po, pq, pt, pl = _queries_at(out, q, k_pages.dtype, block_tables, seq_lens, N, H_q, Dh, dev)
     i32 = _torch.int32
     rc = lib().paged_prefill_attention_mod(
-        po, pq, _at(q_start, dev, "q_start", (B + 1,), i32), int(max_q_len), kp, vp, pt, mb, pl, B, H_q, H_kv, Dh, P,
-        num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
+        po, pq, _at(q_start, dev, "q_start", (B + 1,), i32), int(max_q_len), N, kp, vp, pt, mb, pl, B, H_q, H_kv, Dh,
+        P, num_pages, float(scale), _torch_dtype_code(k_pages), float(softcap),
         _at(alibi_slopes, dev, "alibi_slopes", (H_q,), _torch.float32), int(window),
         _at(key_start, dev, "key_start", (N,), i32), _at(prefix_lens, dev, "prefix_lens", (B,), i32),
         _flag_at(err_flag, dev), _raw_stream(stream, dev))

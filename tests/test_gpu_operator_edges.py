@@ -297,3 +297,24 @@ def test_decode_mod_hidden_keys_have_no_effect(mod, num_splits):
         for t in range(t1):
             M._put(c, s, t, None, 300.0)
     assert np.array_equal(first, M._decode(c, q, 128**-0.5, num_splits, key_start=[3, 44, 2], **mod))
+
+
+@pytest.mark.parametrize("B", [1, 33, 200])
+@pytest.mark.parametrize("dtype,Dh,H_q,H_kv,mod", [("bf16", 128, 8, 2, dict(softcap=30.0)), ("fp16", 128, 8, 8, dict(window=70)),
+                                                   ("bf16", 64, 12, 4, dict(softcap=4.0)), ("bf16", 128, 64, 1, dict(softcap=9.0))])
+def test_prefill_mod_one_long_chunk_among_short_ones(dtype, Dh, H_q, H_kv, mod, B):
+    """Tiles lie behind one another whatever the chunks' lengths are: one long chunk, chunks of one token, empty ones."""
+    rng = np.random.default_rng(B)
+    chunks = rng.integers(0, 3, B)
+    chunks[B // 3] = 401
+    lens = chunks + rng.integers(0, 90, B)
+    c = M._cache(lens, H_kv, Dh, 16, dtype, seed=B)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b), H_q, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = M._prefill(c, q, chunks, Dh**-0.5, err=err, **mod)
+    assert int(err) == 0 and np.isfinite(got).all()
+    rows = np.unique(np.r_[0, len(b) - 1, start[B // 3], start[B // 3 + 1] - 1, rng.integers(0, len(b), 40)])
+    ref, top = M._reference(c, q[torch.from_numpy(rows).cuda()], b[rows], pos[rows], Dh**-0.5, mod.get("softcap", 0.0), None,
+                            mod.get("window", 0))
+    M._close(got[rows], ref, top, "mixed chunks")

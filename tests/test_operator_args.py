@@ -112,7 +112,7 @@ def test_modified_attention_refusals():
     def decode(**kw):
         return L.paged_decode_attention_mod(*{**base, **kw}.values())
 
-    base_p = dict(out=PTR, q=PTR, qs=PTR, mq=4, kp=PTR, vp=PTR, tab=PTR, mb=16, lens=PTR, B=0, Hq=8, H=2, Dh=128, P=16,
+    base_p = dict(out=PTR, q=PTR, qs=PTR, mq=4, nr=4, kp=PTR, vp=PTR, tab=PTR, mb=16, lens=PTR, B=0, Hq=8, H=2, Dh=128, P=16,
                   n=10, scale=0.1, dt=1, cap=0.0, slopes=None, window=0, ks=None, pl=None, err=None, st=None)
 
     def prefill(**kw):
@@ -130,6 +130,7 @@ def test_modified_attention_refusals():
         assert f(B=1, n=1 << 27) == K.KV_ERR_UNSUPPORTED
     assert decode(S=-1) == K.KV_ERR_ARG
     assert prefill(mq=-1) == K.KV_ERR_ARG and prefill(B=1, mq=0) == K.KV_OK
+    assert prefill(nr=-1) == K.KV_ERR_ARG and prefill(B=1, nr=0) == K.KV_OK
     K.paged_decode_set_kernel(K.KV_DECODE_KERNEL_SIMT)  # the selection does not limit the groups of these entry points
     try:
         assert decode(Hq=100, H=2) == K.KV_OK
