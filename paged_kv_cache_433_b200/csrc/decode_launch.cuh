@@ -165,9 +165,9 @@ cudaError_t launch_cols_mod(const DecodeParams& p, const CUtensorMap& tk, const 
 // Multi-token query with modified scores and masks (prefill_mma_mod.cu, prefill_mod_tc.cu).
 cudaError_t launch_prefill_tc_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int P,
                                   dim3 grid, cudaStream_t st);
-// The same with one softmax reference (prefill_cap_tc.cu): n_tiles tiles, `slots` to a KV head.
-cudaError_t launch_prefill_cap_tc(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int P, int slots,
-                                  int n_tiles, cudaStream_t st);
+// The same with one softmax reference (prefill_cap_tc.cu): n_tiles tiles.
+cudaError_t launch_prefill_cap_tc(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int P, int n_tiles,
+                                  cudaStream_t st);
 cudaError_t launch_prefill_mod(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int dtype, int DH,
                                int P, dim3 grid, cudaStream_t st);
 

@@ -177,12 +177,13 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
     int qs0 = 0, n_q = 1, t0 = 0, nt = 1;
     if constexpr (QM) {
         split = 0;
-        kvh = blockIdx.y;
         chunk_pages = 0;
         if constexpr (MOD) {
-            const ChunkTile ct = chunk_tile(p, blockIdx.x, threadIdx.x & 31);
+            const ChunkTile ct = chunk_tile(p, (gridDim.x - 1 - blockIdx.x) / p.H_kv, threadIdx.x & 31);
+            kvh = blockIdx.x % p.H_kv;
             b = ct.b, qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
         } else {
+            kvh = blockIdx.y;
             b = blockIdx.z;
             qs0 = p.q_start[b];
             n_q = p.q_start[b + 1] - qs0;

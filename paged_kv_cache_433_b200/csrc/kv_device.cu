@@ -1041,15 +1041,17 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
     const int64_t rows = static_cast<int64_t>(num_pages) * H_kv * page_size;
     if (!make_pool_map(&tk, k_pages, dtype, rows, Dh, page_size) || !make_pool_map(&tv, v_pages, dtype, rows, Dh, page_size))
         return KV_ERR_CUDA;
-    // mod: the tiles of all sequences behind one another (chunk_tile in score_mod.cuh)
-    const dim3 grid(static_cast<unsigned>(mod ? mod->n_rows / q_tile + B : (max_q_len + q_tile - 1) / q_tile),
-                    static_cast<unsigned>(H_kv), static_cast<unsigned>(mod ? 1 : B));
-    const int64_t n_tiles = static_cast<int64_t>(grid.x) * grid.y;
-    fixed_ref = fixed_ref && tc && n_tiles < (1LL << 31);
+    dim3 grid(static_cast<unsigned>((max_q_len + q_tile - 1) / q_tile), static_cast<unsigned>(H_kv),
+              static_cast<unsigned>(B));
+    if (mod) {  // the tiles of all sequences behind one another (chunk_tile in score_mod.cuh)
+        const int64_t n_tiles = (static_cast<int64_t>(mod->n_rows) / q_tile + B) * H_kv;
+        if (n_tiles >= (1LL << 31)) return KV_ERR_UNSUPPORTED;
+        grid = dim3(static_cast<unsigned>(n_tiles));
+    }
+    fixed_ref = fixed_ref && tc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = mod && !tc               ? launch_prefill_mod(p, tk, tv, dtype, Dh, page_size, grid, st)
-                          : fixed_ref              ? launch_prefill_cap_tc(p, tk, tv, page_size, static_cast<int>(grid.x),
-                                                                           static_cast<int>(n_tiles), st)
+                          : fixed_ref              ? launch_prefill_cap_tc(p, tk, tv, page_size, static_cast<int>(grid.x), st)
                           : mod                    ? launch_prefill_tc_mod(p, tk, tv, dtype, page_size, grid, st)
                           : tc                     ? launch_prefill_tc(p, tk, tv, dtype, page_size, grid, st)
                           : dtype == KV_DTYPE_BF16 ? launch_prefill_bf16(p, tk, tv, Dh, page_size, grid, st)

@@ -3,10 +3,10 @@
 
 namespace kvp {
 
-cudaError_t launch_prefill_cap_tc(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int P, int slots,
-                                  int n_tiles, cudaStream_t st) {
-    return P == 16 ? launch_prefill_cap_tc_inst<16>(p, tk, tv, slots, n_tiles, st)
-                   : launch_prefill_cap_tc_inst<32>(p, tk, tv, slots, n_tiles, st);
+cudaError_t launch_prefill_cap_tc(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int P, int n_tiles,
+                                  cudaStream_t st) {
+    return P == 16 ? launch_prefill_cap_tc_inst<16>(p, tk, tv, n_tiles, st)
+                   : launch_prefill_cap_tc_inst<32>(p, tk, tv, n_tiles, st);
 }
 
 }  // namespace kvp

@@ -87,12 +87,12 @@ struct CapTile {
 };
 static_assert(sizeof(CapTile) <= 32 * 4, "description of a tile");
 template <int P>
-__device__ __forceinline__ CapTile cap_tile(const DecodeParams& p, int tile, int slots, int lane) {
+__device__ __forceinline__ CapTile cap_tile(const DecodeParams& p, int tile, int n_tiles, int lane) {
     constexpr int kTP = PfCapCfg<P>::kTP;
     CapTile t;
     t.tile = tile;
-    const ChunkTile ct = chunk_tile(p, tile % slots, lane);
-    t.kvh = tile / slots;
+    const ChunkTile ct = chunk_tile(p, (n_tiles - 1 - tile) / p.H_kv, lane);
+    t.kvh = tile % p.H_kv;
     t.b = ct.b;
     t.qs0 = ct.qs0;
     const int n_q = ct.n_q, len = p.seq_lens[t.b];
@@ -142,13 +142,14 @@ __device__ __forceinline__ uint32_t bits32_below(int n) { return n <= 0 ? 0u : n
 template <int P>
 __global__ void __launch_bounds__(512, 1)
     paged_prefill_cap_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmap_k,
-                                const __grid_constant__ CUtensorMap tmap_v, const int slots) {
+                                const __grid_constant__ CUtensorMap tmap_v) {
     using C = PfCapCfg<P>;
     constexpr int DH = C::kDH, kTP = C::kTP, kG = C::kGroups;
     constexpr uint32_t kIdescQK = idesc_f16(true, 128, kTP, false, false);
     constexpr uint32_t kIdescPV = idesc_f16(true, 128, DH, false, true);
     constexpr int kFlush = kFlushKeys / kTP;  // stages whose P.V share one accumulation
     extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int n_tiles = gridDim.x;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(512, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 int* d = reinterpret_cast<int*>(smem + C::kOffTiles) + slot * C::kTileWords;
-                if (tile >= 0) t = cap_tile<P>(p, tile, slots, lane);
+                if (tile >= 0) t = cap_tile<P>(p, tile, n_tiles, lane);
                 t.tile = tile;
                 if (lane == 0) *reinterpret_cast<CapTile*>(d) = t;
                 for (int i = lane; tile >= 0 && !t.bad_len && i < t.nt; i += 32)
@@ -529,8 +530,8 @@ __global__ void __launch_bounds__(512, 1)
                         *reinterpret_cast<float4*>(dst + q * 16 + i) =
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
                     if (again && l == l && ok) {
-                        const ChunkTile ct = chunk_tile(p, last_tile % slots);
-                        const int b = ct.b, kvh = last_tile / slots, i0 = ct.t0 + tr, len = p.seq_lens[b];
+                        const ChunkTile ct = chunk_tile(p, (n_tiles - 1 - last_tile) / p.H_kv);
+                        const int b = ct.b, kvh = last_tile % p.H_kv, i0 = ct.t0 + tr, len = p.seq_lens[b];
                         const int pos = len - ct.n_q + i0;
                         const int lo = first_key(p, ct.qs0 + i0, pos);
                         const int hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0);
@@ -727,8 +728,8 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 template <int P>
-cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int slots,
-                                       int n_tiles, cudaStream_t st) {
+cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int n_tiles,
+                                       cudaStream_t st) {
     using C = PfCapCfg<P>;
     auto* kern = paged_prefill_cap_tc_kernel<P>;
     static std::atomic<uint64_t> configured{0};
@@ -741,7 +742,7 @@ cudaError_t launch_prefill_cap_tc_inst(const DecodeParams& p, const CUtensorMap&
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_pdl(kern, dim3(static_cast<unsigned>(n_tiles)), dim3(C::kThreads), C::kSmem, st, p, tk, tv, slots);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(n_tiles)), dim3(C::kThreads), C::kSmem, st, p, tk, tv);
 }
 
 }  // namespace kvp

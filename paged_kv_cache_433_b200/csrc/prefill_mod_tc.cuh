@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0) grid_launch_dependents();
 
     // ---- this CTA's tile: chunk tokens t0 .. t0 + nt - 1 of sequence b, KV head kvh
-    const ChunkTile ct = chunk_tile(p, blockIdx.x, lane);
-    const int kvh = blockIdx.y, b = ct.b;
+    const ChunkTile ct = chunk_tile(p, (gridDim.x - 1 - blockIdx.x) / p.H_kv, lane);
+    const int kvh = blockIdx.x % p.H_kv, b = ct.b;
     const int g = p.g;
     const int qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
     if (t0 >= n_q) return;
