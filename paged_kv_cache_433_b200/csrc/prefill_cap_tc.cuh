@@ -19,9 +19,9 @@
 // ahead into it, and a warpgroup computes its first stage of it before it reads out O of the last one, for which it has to
 // wait for the slowest. A tile's start and end, about 10 us with a CTA each, are hidden that way -- windowed layers have few stages per tile.
 //
-// Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 435 us, 672 TFLOP/s counted once, 1008 with the
+// Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 430 us, 680 TFLOP/s counted once, 1020 with the
 // residuals' products (a CTA per tile: 475 us; without the cap, prefill_tc.cuh: 425-430). Two prompts of 4096 tokens in
-// documents of 1500 under a window of 1024, cap 30: 300 us (a CTA per tile: 340). Bound by the chain Q K^T -> softmax ->
+// documents of 1500 under a window of 1024, cap 30: 260 us (a CTA per tile, ascending: 340). Bound by the chain Q K^T -> softmax ->
 // P V of a stage, about 10,400 cycles at three stages in flight: the matrix pipe is busy for 1,536 cycles a stage, the
 // exponentials for 1,024, and tensor memory has no room for a fourth buffer of scores.
 //
