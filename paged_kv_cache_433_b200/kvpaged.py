@@ -463,7 +463,7 @@ def _begin(t, name: str) -> int:
 
         _torch = torch
     dev = t.get_device()
-    if dev < 0 or dev != _torch.cuda.current_device():
+    if dev < 0 or dev != _torch._C._cuda_getDevice():  # (a CUDA tensor exists: the runtime is up)
         raise ValueError(f"{name} must be a tensor on the current CUDA device")
     return dev
 
@@ -508,14 +508,18 @@ def _token_stride(t, name: str, H: int, Dh: int) -> int:
 def _flag_at(err_flag, dev: int):
     if err_flag is None:
         return None
+    if err_flag.get_device() != dev or err_flag.dtype != _torch.int32:
+        _refuse(dev, (err_flag, "err_flag", err_flag.shape, _torch.int32, True))
     _need(err_flag.numel() >= 1, "err_flag is empty")
-    return _at(err_flag, dev, "err_flag", err_flag.shape, _torch.int32)
+    return err_flag.data_ptr()
 
 
 def _scratch_at(workspace, dev: int):
     if workspace is None:
         return None, 0
-    return _at(workspace, dev, "workspace", workspace.shape, workspace.dtype), workspace.nbytes
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(dev, (workspace, "workspace", workspace.shape, workspace.dtype))
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _raw_stream(stream, dev: int) -> int:
