@@ -61,9 +61,11 @@ __device__ __forceinline__ uint4 quantise16(const float (&x)[16], int32_t cpr, u
 // One thread takes the same sixteen elements of a token's K and V row (one 16-byte vector of codes each): four loads in
 // flight, issued beside that of the slot. Bound by memory: 8185 tokens of 8 heads of 128 (bf16) take 14.7 us, 3.4 TB/s (0.52
 // of the measured copy rate, at a size where a launch's start and end weigh as much as its middle); 15.4 us with a thread
-// per K or V vector and the slot read first.
+// per K or V vector and the slot read first. CTAs of 128: with 256 the append and the read-back behind it take 26.4 us for
+// 25.9.
+constexpr int kAppendThreads = 128;
 template <int DT>
-__global__ void __launch_bounds__(256) kv_append_int8_kernel(uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
+__global__ void __launch_bounds__(kAppendThreads) kv_append_int8_kernel(uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
                                                              float* __restrict__ scales, const uint4* __restrict__ k_new,
                                                              const uint4* __restrict__ v_new, int64_t k_stride,
                                                              int64_t v_stride, const int64_t* __restrict__ slots,
@@ -213,10 +215,10 @@ int kv_append_int8(void* k_pages, void* v_pages, float* kv_scales, const void* k
     int32_t lg = 0;
     while ((16 << lg) < Dh) ++lg;
     const int64_t per = static_cast<int64_t>(B) * H_kv << lg;
-    const int64_t blocks = (per + 255) / 256;
+    const int64_t blocks = (per + kAppendThreads - 1) / kAppendThreads;
     if (blocks > 0x7fffffffLL) return KV_ERR_UNSUPPORTED;
     auto run = [&](auto kernel) {
-        return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream),
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0, static_cast<cudaStream_t>(stream),
                           static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages), kv_scales,
                           static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), k_stride / N, v_stride / N,
                           slot_mapping, per, H_kv, lg, page_size, static_cast<int64_t>(num_pages) * page_size, err_flag);
