@@ -476,26 +476,37 @@ int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_bl
 }
 
 int check_mod(float softcap, int32_t window) {
-    return softcap >= 0.f && softcap < 3.0e38f && window >= 0 ? KV_OK : KV_ERR_ARG;  // a NaN fails the comparison
+    return softcap >= 0.f && std::isfinite(softcap) && window >= 0 ? KV_OK : KV_ERR_ARG;  // a NaN fails the comparison
+}
+
+// Coefficients poly[k] (scale / c)^2k scale log2 e of the capped score as a polynomial in the square of the product
+// x = q . k (score_mod.cuh), and the largest |x| that they serve (negative: none): |u| = |x scale / c| <= top. Under a
+// large cap the powers of scale / c leave fp32's range one after another; coefficients below it are left out, and the
+// polynomial then serves only |u| whose omitted terms are below 3e-8 of the score. x^2 has to stay in range as well.
+float cap_poly(double scale, double c, const double* poly, int n, double top, float* coef) {
+    const double u = scale / c;
+    double f = scale * 1.4426950408889634;
+    bool ok = u != 0.;
+    for (int k = 0; k < n; ++k, f *= u * u) {
+        const double a = std::abs(poly[k] * f);
+        const bool out = a < 1.2e-38;
+        coef[k] = out ? 0.f : static_cast<float>(poly[k] * f);
+        ok = ok && a < 1e30 && (k > 0 || !out);
+        if (out && k > 0) top = std::min(top, std::pow(3e-8 / std::abs(poly[k]), 0.5 / k));
+    }
+    return ok ? static_cast<float>(std::min(top / std::abs(u), 1e18)) : -1.f;
 }
 
 void set_mod(DecodeParams& p, float scale, float softcap, const float* alibi_slopes, int32_t window,
              const int32_t* key_start) {
-    p.cap_in = softcap > 0.f ? scale / softcap : 0.f;
-    p.cap_out = softcap * kLog2e;
-    // the polynomial of the capped score in the square of the product q . k (score_mod.cuh); where its
-    // coefficients leave fp32's range every score takes the exponential form
-    const double u = p.cap_in, o = static_cast<double>(scale) * 1.4426950408889634;
-    double f = o, top = 0.;
-    for (int i = 0; i < kCapTerms; ++i, f *= u * u) {
-        p.cap_coef[i] = static_cast<float>(kTanhPoly[i] * f);
-        top = std::max(top, std::abs(kTanhPoly[i] * f));
+    // a cap above 1e36 (scale / c may leave fp32's range) changes no score below 1e35
+    if (softcap > 0.f && softcap <= 1e36f) {
+        constexpr double kMax = 3.4e38;
+        p.cap_in = static_cast<float>(std::clamp(static_cast<double>(scale) / softcap, -kMax, kMax));
+        p.cap_out = std::max(softcap * kLog2e, 1.2e-38f);  // (0 would mean none)
+        p.cap_small = cap_poly(scale, softcap, kTanhPoly, kCapTerms, kTanhSmall, p.cap_coef);
+        p.cap_tiny = cap_poly(scale, softcap, kTanhTinyPoly, kCapTinyTerms, kTanhTiny, p.cap_coef_tiny);
     }
-    const bool poly = u != 0. && top < 1e30 && kTanhSmall / std::abs(u) < 1e15;
-    p.cap_small = poly ? static_cast<float>(kTanhSmall / std::abs(u)) : -1.f;
-    p.cap_tiny = poly ? static_cast<float>(kTanhTiny / std::abs(u)) : -1.f;
-    f = o;
-    for (int i = 0; i < kCapTinyTerms; ++i, f *= u * u) p.cap_coef_tiny[i] = static_cast<float>(kTanhTinyPoly[i] * f);
     p.alibi_slopes = alibi_slopes;
     p.window = window;
     p.key_start = key_start;
@@ -1034,7 +1045,7 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
         // A cap bounds every score by cap_out; where 2^(2 cap_out) fits fp32's range with room on both sides (bf16
         // operands have that range too) and no bias moves the scores, one reference serves all rows: no row maximum is
         // taken.
-        fixed_ref = dtype == KV_DTYPE_BF16 && mod->softcap > 0.f && p.cap_out <= kFixedRefMax && !mod->alibi_slopes;
+        fixed_ref = dtype == KV_DTYPE_BF16 && p.cap_out > 0.f && p.cap_out <= kFixedRefMax && !mod->alibi_slopes;
         p.fixed_ref = std::max(0.f, p.cap_out - kFixedTop);
     }
     CUtensorMap tk, tv;

@@ -93,11 +93,6 @@ __device__ __forceinline__ TileKeys tile_keys(const DecodeParams& p, int row0, i
     return k;
 }
 
-// tanh(u) = 1 - 2 / (1 + e^2u): absolute error about 1e-7 for every u (+-inf give +-1).
-__device__ __forceinline__ float tanh_any(float u) {
-    return 1.f - 2.f * __frcp_rn(1.f + exp2f(u * 2.885390081777927f));
-}
-
 // Where |u| <= kTanhSmall: tanh(u) = u * P(u^2), P of degree 5 fitted to tanh(u) / u by least squares reweighted
 // towards equal relative errors (2.9e-8). No special-function unit, and relative instead of absolute accuracy:
 // scores that are small beside the cap, the usual case, keep all their bits. With u = x * scale / c for a product
@@ -116,6 +111,16 @@ constexpr double kTanhPoly[kCapTerms] = {0.999999971, -0.333329589, 0.13325406, 
 constexpr int kCapTinyTerms = 3;
 constexpr double kTanhTiny = 0.2;
 constexpr double kTanhTinyPoly[kCapTinyTerms] = {0.999999895, -0.333285909, 0.130154075};
+// tanh(u) of any u: beyond kTanhSmall 1 - 2 / (1 + e^2u), whose error is 1e-7 of 1 (+-inf give +-1). That would be
+// anything but small beside a small u, which a cap far above the scores makes of all of them; the polynomial is there too.
+__device__ __forceinline__ float tanh_any(float u) {
+    constexpr float c[kCapTerms] = {kTanhPoly[0], kTanhPoly[1], kTanhPoly[2], kTanhPoly[3], kTanhPoly[4], kTanhPoly[5]};
+    const float z = u * u;
+    float r = c[kCapTerms - 1];
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, c[i]);
+    return fabsf(u) <= static_cast<float>(kTanhSmall) ? u * r : 1.f - 2.f * __frcp_rn(1.f + exp2f(u * 2.885390081777927f));
+}
 // Chunked prefill: the largest cap (log2 units; 50 in natural ones) with one softmax reference for all rows, and the
 // largest power of two that its probabilities then reach: they lie in 2^-96 .. 2^50, a residual of 16-bit splitting 2^9
 // lower, so that sums with values from 1e-6 to 1e17 stay inside the normal range.

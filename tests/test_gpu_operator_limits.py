@@ -1,0 +1,81 @@
+"""The modified-score and int8 entry points at the ends of what they document: caps of every size, tables whose entries
+before the first visible key are gone, infinities and overflow in V, rows past n_rows, the widest tables."""
+import numpy as np
+import pytest
+import test_gpu_score_mod as M
+import torch
+
+from paged_kv_cache_433_b200 import kvpaged as K
+
+pytestmark = pytest.mark.gpu
+
+# the kernels of paged_prefill_attention_mod: one softmax reference (bf16, cap <= 50), general tcgen05, warp MMA
+PREFILL = [("bf16", 128, None), ("fp16", 128, None), ("bf16", 128, K.KV_DECODE_KERNEL_MMA), ("fp16", 64, None)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_433_b200 import build
+
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def _with_kernel(kernel, run):
+    if kernel is not None:
+        K.paged_decode_set_kernel(kernel)
+    try:
+        return run()
+    finally:
+        K.paged_decode_set_kernel(K.KV_DECODE_KERNEL_AUTO)
+
+
+# ------------------------------------------------------------------ caps
+CAPS = [1e-30, 1e-3, 600.0, 1e4, 1e10, 1e13, 1e14, 1e15, 1e20, 1e30, 1e36, 2.9e38, float(np.finfo(np.float32).max)]
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("dtype,Dh,P", [("bf16", 128, 16), ("fp16", 64, 32)])
+def test_decode_mod_caps_of_every_size(dtype, Dh, P, cap):
+    lens = [300, 1, 70]
+    c = M._cache(lens, 2, Dh, P, dtype, seed=1)
+    q = (2 * torch.randn((3, 8, Dh), generator=c["g"], device="cuda")).to(M.DT[dtype])
+    ref, top = M._reference(c, q, np.arange(3), np.array(lens) - 1, Dh**-0.5, cap)
+    for S in (1, 0):
+        M._close(M._decode(c, q, Dh**-0.5, S, softcap=cap), ref, top, f"cap {cap}")
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("dtype,Dh,kernel", PREFILL)
+def test_prefill_mod_caps_of_every_size(dtype, Dh, kernel, cap):
+    lens, chunks = [300, 90], np.array([40, 90])
+    c = M._cache(lens, 2, Dh, 16, dtype, seed=2)
+    b, pos, _ = M._rows(lens, chunks)
+    q = (2 * torch.randn((len(b), 8, Dh), generator=c["g"], device="cuda")).to(M.DT[dtype])
+    ref, top = M._reference(c, q, b, pos, Dh**-0.5, cap)
+    got = _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, softcap=cap))
+    M._close(got, ref, top, f"cap {cap}")
+
+
+@pytest.mark.parametrize("cap", [700.0, 1e5, 1e16])
+@pytest.mark.parametrize("scale", [128**-0.5, 1e-6, 2e3])
+def test_decode_mod_scores_below_at_and_above_a_large_cap(cap, scale):
+    """Products of one, two, ... steps of a size, over the whole rise of the tanh: with slopes that hold the cap's multiples
+    against one another every key keeps a weight, so that each capped score shows. A score of size s in log2 units errs by
+    2^-21 s (a few roundings of 2^-24 and 2^-23), a weight by that times log 2, and so the row's sum over |v| <= top."""
+    n, Dh = 12, 128
+    c = M._cache([n], 1, Dh, 16, "bf16", seed=3)
+    size = 2.0 ** np.round(np.log2(0.25 * cap / scale))  # the products k * size, k = 1 .. n, are exact
+    c["kp"][int(c["tab"][0, 0]), 0] = 0
+    c["kp"][int(c["tab"][0, 0]), 0, :n, 0] = torch.arange(1, n + 1, device="cuda", dtype=torch.float32) * float(2.0 ** (np.log2(size) // 2))
+    q = torch.zeros((1, 1, Dh), device="cuda", dtype=torch.bfloat16)
+    q[0, 0, 0] = float(size / 2.0 ** (np.log2(size) // 2))
+    s = cap * np.tanh(np.arange(1, n + 1) * size * scale / cap)
+    # the last keys of the rise are level; the slope brings key 3 up to key 8
+    slope = -(s[7] - s[2]) / 5
+    ref, top = M._reference(c, q, np.zeros(1, int), np.array([n - 1]), scale, cap, torch.tensor([slope], dtype=torch.float32))
+    got = M._decode(c, q, scale, 1, softcap=cap, alibi_slopes=torch.tensor([slope], dtype=torch.float32, device="cuda"))
+    if 2.0**-21 * 1.45 * cap < 0.5:
+        assert np.abs(got - ref).max() <= (2.0**-13 + 2.0**-21 * 1.45 * (cap + 11 * abs(slope))) * top.max()
+    else:  # scores so far apart that one key has the whole weight
+        assert np.isfinite(got).all()
