@@ -280,6 +280,8 @@ __global__ void __launch_bounds__(512, 1)
             if (t.tile < 0) break;
             const int32_t* row = p.block_tables + (int64_t)t.b * p.max_blocks + t.page_first;
             int tab_cur = lane < t.n_pages ? row[lane] : -1, tab_nxt = -1;
+            // pages of the first stage that lie before the first key any row sees: not loaded, whatever their entries are
+            const int skip = t.k.begin / P - t.page_first;
             for (int j = 0; j < t.n_st; ++j) {
                 const int np = min(C::kPPS, t.n_pages - j * C::kPPS);
                 // block-table entries come 32 at a time, one per lane, the next 32 fetched while these are used
@@ -290,9 +292,10 @@ __global__ void __launch_bounds__(512, 1)
                     tab_nxt = (base + 32 + lane < t.n_pages) ? row[base + 32 + lane] : -1;
                 }
                 const int pg_all = __shfl_sync(0xffffffffu, tab_cur, (j * C::kPPS + lane) & 31);
-                const int pg = lane < np ? pg_all : -1;
-                const bool good = lane < np && pg >= 0 && pg < p.num_pages;
-                if (lane < np && !good) raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
+                const bool wanted = lane < np && j * C::kPPS + lane >= skip;
+                const int pg = wanted ? pg_all : -1;
+                const bool good = wanted && pg >= 0 && pg < p.num_pages;
+                if (wanted && !good) raise_err(p.err, KV_DEV_ERR_PAGE_RANGE);
                 const unsigned gmask = __ballot_sync(0xffffffffu, good);
                 const int box_page = lane / C::kBoxCols, bb = lane % C::kBoxCols;
                 const int pgl = __shfl_sync(0xffffffffu, pg, box_page & 31);

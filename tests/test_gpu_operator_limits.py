@@ -79,3 +79,29 @@ def test_decode_mod_scores_below_at_and_above_a_large_cap(cap, scale):
         assert np.abs(got - ref).max() <= (2.0**-13 + 2.0**-21 * 1.45 * (cap + 11 * abs(slope))) * top.max()
     else:  # scores so far apart that one key has the whole weight
         assert np.isfinite(got).all()
+
+
+# ------------------------------------------------------------------ pages behind a window are gone
+@pytest.mark.parametrize("gone", [-1, 10**6])
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("dtype,Dh,kernel,mod", [
+    ("bf16", 128, None, dict(softcap=30.0)), ("bf16", 128, None, dict()), ("fp16", 128, None, dict(softcap=30.0)),
+    ("bf16", 128, K.KV_DECODE_KERNEL_MMA, dict()), ("fp16", 64, None, dict())], ids=str)
+def test_prefill_mod_skips_pages_before_the_window(dtype, Dh, kernel, mod, P, gone):
+    """Table entries of pages that no row of a chunk sees may be anything, and are no error."""
+    lens, chunks = [700, 333, 90, 1000], np.array([100, 1, 90, 33])
+    c = M._cache(lens, 2, Dh, P, dtype, seed=6)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b), 8, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    ks = np.where(b == 3, 970, 0)  # a document that begins inside the last chunk's window
+    ref, top = M._reference(c, q, b, pos, Dh**-0.5, mod.get("softcap", 0.0), None, 75, ks)
+    for i in range(4):
+        first = max(0, lens[i] - chunks[i] - 75 + 1, 970 if i == 3 else 0)
+        c["tab"][i, :first // P] = gone
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, ks, err=err, window=75, **mod))
+    M._close(got, ref, top, "pages gone")
+    assert int(err) == 0
+    c["tab"][3, -1] = gone  # one that is seen is reported
+    _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, ks, err=err, window=75, **mod))
+    assert int(err) == K.KV_DEV_ERR_PAGE_RANGE
