@@ -493,8 +493,11 @@ int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32
  * that a row does not see have no effect on it, whatever they hold (NaN and
  * infinities in K and V included: not a bit of the row depends on them); a NaN
  * among the scores or values it sees gives NaN, an infinity among the values
- * its sign. Pages before the first visible key are not read (their table
- * entries may be anything).
+ * its sign. Weighted sums are fp32, of weights up to 2^8 (2^50 in the chunk
+ * form's kernel for bf16 under a cap of at most 50): where the |V| of a dim that
+ * a row sees add up to more than 2^119 (2^77), it may come out infinite or NaN.
+ * Pages before the first visible key are not read (their table entries may be
+ * anything).
  * softcap: 0 (none) or positive and finite (above 1e36 as none); window: 0 (none) or positive.
  * bf16 / fp16 K/V, H_q / H_kv <= 64, Dh in {64, 128}, page_size in {16, 32},
  * num_pages * H_kv * page_size < 2^31. */

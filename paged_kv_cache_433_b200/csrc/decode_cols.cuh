@@ -773,9 +773,11 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                     // An infinity among the visible values meets a probability's residual, which may be 0 or negative:
                     // a NaN. Where a sum is NaN and the weights are not (rare), the values say what it is.
                     if constexpr (MOD)
-                        if (x[h] != x[h] && L == L)
-                            x[h] = sum_nonfinite<kPBF16>(p, b, kvh, P, DH, m * 16 + h * 8 + r0, max(pc.key_begin, tok0),
-                                                         min(len, tok0 + pc.n * P));
+                        if (x[h] != x[h] && L == L) {
+                            const float f = sum_nonfinite<kPBF16>(p, b, kvh, P, DH, m * 16 + h * 8 + r0,
+                                                                  max(pc.key_begin, tok0), min(len, tok0 + pc.n * P));
+                            if (f != 0.f) x[h] = f;  // (0: finite values whose weighted sum left fp32)
+                        }
                     x[h] = whole && L == 0.f ? 0.f : x[h] * scale;
                 }
                 if constexpr (kI8) {

@@ -805,7 +805,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
             // a NaN. Where a sum is NaN and the weights are not (rare), the row's values say what it is.
             if (U != U && L == L) {
                 const int tr = hh / p.g, pos = len - n_q + t0 + tr;
-                U = sum_nonfinite<kBF16>(p, b, kvh, P, DH, d, first_key(p, qs0 + t0 + tr, pos), max(pos + 1, prefix));
+                const float f = sum_nonfinite<kBF16>(p, b, kvh, P, DH, d, first_key(p, qs0 + t0 + tr, pos), max(pos + 1, prefix));
+                if (f != 0.f) U = f;  // (0: finite values whose weighted sum left fp32)
             }
         }
         if (!split_mode) {

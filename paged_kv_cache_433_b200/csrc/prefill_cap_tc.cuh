@@ -540,9 +540,9 @@ __global__ void __launch_bounds__(512, 1)
                         const int hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0);
 #pragma unroll 1
                         for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<true>(p, b, kvh, P, DH, od + q * 16 + i, lo, hi) * inv;
+                            const float x = sum_nonfinite<true>(p, b, kvh, P, DH, od + q * 16 + i, lo, hi);
                             float& y = dst[q * 16 + i];
-                            y = y != y ? x : y + x;
+                            if (x != 0.f) y = y != y ? x * inv : y + x * inv;  // (0: finite values whose weighted sum left fp32)
                         }
                     }
                 }

@@ -581,9 +581,9 @@ __global__ void __launch_bounds__(384, 1)
                     if (again && l_all == l_all) {
 #pragma unroll 1
                         for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi) * inv;
+                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi);
                             float& y = dst[q * 16 + i];
-                            y = y != y ? x : y + x;
+                            if (x != 0.f) y = y != y ? x * inv : y + x * inv;  // (0: finite values whose weighted sum left fp32)
                         }
                     }
                 }

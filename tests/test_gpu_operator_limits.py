@@ -105,3 +105,28 @@ def test_prefill_mod_skips_pages_before_the_window(dtype, Dh, kernel, mod, P, go
     c["tab"][3, -1] = gone  # one that is seen is reported
     _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, ks, err=err, window=75, **mod))
     assert int(err) == K.KV_DEV_ERR_PAGE_RANGE
+
+
+# ------------------------------------------------------------------ finite values that overflow
+@pytest.mark.parametrize("kernel", [None, K.KV_DECODE_KERNEL_MMA])
+@pytest.mark.parametrize("size,cap", [(1e30, 50.0), (3.3e38, 50.0), (3.3e38, 60.0), (3.3e38, 0.0)])
+def test_prefill_mod_finite_values_that_overflow(size, cap, kernel):
+    """Finite values whose weighted sum leaves fp32 give an infinity or not a number, never another finite value."""
+    c = M._cache([300], 1, 128, 16, "bf16", seed=5)
+    c["kp"] = c["kp"].abs()
+    c["vp"].fill_(size)
+    q = (500 * torch.randn((40, 4, 128), generator=c["g"], device="cuda").abs()).to(torch.bfloat16)
+    got = _with_kernel(kernel, lambda: M._prefill(c, q, np.array([40]), 128**-0.5, softcap=cap))
+    fine = np.isfinite(got)
+    assert (np.abs(got[fine] / size - 1) < 2.0**-7).all()
+
+
+@pytest.mark.parametrize("num_splits", [1, 0, 3])
+def test_decode_mod_finite_values_that_overflow(num_splits):
+    c = M._cache([2000], 1, 128, 16, "bf16", seed=5)
+    q = (2 * torch.randn((1, 8, 128), generator=c["g"], device="cuda")).to(torch.bfloat16)
+    c["vp"].copy_(3.3e38 * torch.sign(c["vp"].float()))
+    got = M._decode(c, q, 128**-0.5, num_splits)
+    ref, _ = M._reference(c, q, np.zeros(1, int), np.array([1999]), 128**-0.5)
+    fine = np.isfinite(got)
+    assert (np.abs(got - ref)[fine] < 2.0**-12 * 3.3e38).all()
