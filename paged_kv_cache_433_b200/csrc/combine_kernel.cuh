@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
     constexpr int kPer = 8;      // splits per warp per round
     constexpr int kRound = WPR * kPer;
     constexpr int kRows = kCombineWarps / WPR;
+    auto weight = [](float d) { return MOD ? merge_weight(d) : exp2f(d); };
     __shared__ float red_u[kCombineWarps][DH];
     __shared__ float red_l[kCombineWarps], red_m[kCombineWarps];
     const int warp = threadIdx.x >> 5;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
 #pragma unroll
         for (int j = 0; j < kPer; ++j) mr = fmaxf(mr, st[j].x);
         if (mr > mw) {
-            const float a = mw == -INFINITY ? 0.f : exp2f(mw - mr);
+            const float a = mw == -INFINITY ? 0.f : weight(mw - mr);
             L *= a;
 #pragma unroll
             for (int i = 0; i < kD; ++i) acc[i] *= a;
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 if (st[j].x == -INFINITY) continue;
-                const float w = exp2f(st[j].x - mw);
+                const float w = weight(st[j].x - mw);
                 L += w * st[j].y;
 #pragma unroll
                 for (int i = 0; i < kD; ++i) acc[i] += w * v[j][i];
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
             float Lt = 0.f;
 #pragma unroll
             for (int w = 0; w < WPR; ++w) {
-                sc[w] = red_m[row_w0 + w] == -INFINITY ? 0.f : exp2f(red_m[row_w0 + w] - ms);
+                sc[w] = red_m[row_w0 + w] == -INFINITY ? 0.f : weight(red_m[row_w0 + w] - ms);
                 Lt += sc[w] * red_l[row_w0 + w];
             }
             for (int d = lane; d < DH; d += 32) {

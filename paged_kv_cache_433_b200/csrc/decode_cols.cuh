@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_ker
 #pragma unroll
                 for (int j = 0; j < kRound; ++j) mr = fmaxf(mr, ml[j].x);
                 if (mr == -INFINITY) continue;
-                const float a = m == -INFINITY ? 0.f : exp2f(m - mr);
+                const float a = m == -INFINITY ? 0.f : merge_weight(m - mr);
                 m = mr;
                 L *= a;
 #pragma unroll
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_ker
 #pragma unroll
                 for (int j = 0; j < kRound; ++j) {
                     if (ml[j].x == -INFINITY) continue;
-                    const float w = exp2f(ml[j].x - m);
+                    const float w = merge_weight(ml[j].x - m);
                     L += w * ml[j].y;
 #pragma unroll
                     for (int i = 0; i < kD; ++i) acc[i] += w * x[j][i];
@@ -862,13 +862,13 @@ __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_ker
             if (h < g && part == 0) {
                 float ms = m;
                 for (int w = 1; w < wph; ++w) ms = fmaxf(ms, red_m[warp + w]);
-                const float a = m == -INFINITY ? 0.f : exp2f(m - ms);
+                const float a = m == -INFINITY ? 0.f : merge_weight(m - ms);
                 L *= a;
 #pragma unroll
                 for (int i = 0; i < kD; ++i) acc[i] *= a;
                 for (int w = 1; w < wph; ++w) {
                     if (red_m[warp + w] == -INFINITY) continue;
-                    const float sw = exp2f(red_m[warp + w] - ms);
+                    const float sw = merge_weight(red_m[warp + w] - ms);
                     L += sw * red_l[warp + w];
 #pragma unroll
                     for (int i = 0; i < kD; ++i) acc[i] += sw * red_u[warp + w][lane * kD + i];

@@ -14,6 +14,11 @@ __device__ __forceinline__ int first_visible_key(int pos, int window, const int3
     return lo;
 }
 
+// Weight 2^d (d <= 0) of a partial in a merge of modified-score rows: never 0, so that an infinity in a partial whose
+// scores are far below the others' keeps its sign (0 times it is NaN). What it adds otherwise, 2^-126 of a partial sum,
+// is far below a rounding of the others.
+__device__ __forceinline__ float merge_weight(float d) { return fmaxf(exp2f(d), 1.17549435e-38f); }
+
 constexpr int kPlanHdr = 4;  // header words before the per-sequence arrays
 
 // Balanced plan (paged_plan_stream_kernel): [0] kPlanStream, [1] G | v << 16,

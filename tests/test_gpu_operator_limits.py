@@ -130,3 +130,20 @@ def test_decode_mod_finite_values_that_overflow(num_splits):
     ref, _ = M._reference(c, q, np.zeros(1, int), np.array([1999]), 128**-0.5)
     fine = np.isfinite(got)
     assert (np.abs(got - ref)[fine] < 2.0**-12 * 3.3e38).all()
+
+
+# ------------------------------------------------------------------ infinities
+@pytest.mark.parametrize("num_splits", [1, 2, 0])
+def test_decode_mod_infinity_of_a_vanishing_weight(num_splits):
+    """An infinity among the visible values gives its sign, however small its weight beside another piece's is."""
+    lens = [600, 4000]
+    c = M._cache(lens, 1, 128, 16, "bf16", seed=4)
+    q = torch.randn((2, 4, 128), generator=c["g"], device="cuda").to(torch.bfloat16)
+    for b, L in enumerate(lens):
+        M._put(c, b, L - 3, None, 60 * torch.sign(q[b, 0].float()).to(torch.bfloat16), ("kp",))
+        page, off = int(c["tab"][b, 0]), 5
+        c["vp"][page, 0, off, 7] = float("-inf")
+    q[:, 1:] = q[:, :1]
+    ref, top = M._reference(c, q, np.arange(2), np.array(lens) - 1, 128**-0.5)
+    assert (ref[:, :, 7] == -np.inf).all() and np.isfinite(np.delete(ref, 7, 2)).all()
+    M._close(M._decode(c, q, 128**-0.5, num_splits), ref, top, "infinity")
