@@ -753,16 +753,19 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         o[nt][m][2 * h + e] = o[nt][m][2 * h + e] * sa + src[((nt * kOM + m) * 4 + 2 * h + e) * kLanes] * sb;
             }
     }
+    const bool whole = pc.slot < 0;
+    auto partial = [&](int n) {  // slot of the slice's head n in the partials
+        return balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : ((int64_t)b * p.H_q + head0 + n) * p.num_splits + blockIdx.x;
+    };
+    auto out_row = [&](int n) { return whole ? p.out + ((int64_t)b * p.H_q + head0 + n) * DH : p.part_u + partial(n) * DH; };
+    bool nan = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int n = nt * 8 + 2 * quad + e;
             if (n >= heads) continue;
-            const int64_t hq = (int64_t)b * p.H_q + head0 + n;
-            const bool whole = pc.slot < 0;
-            const int64_t ps = balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : hq * p.num_splits + blockIdx.x;
-            float* dst = whole ? p.out + hq * DH : p.part_u + ps * DH;
+            float* dst = out_row(n);
             const float L = l_col[nt][e], scale = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
 #pragma unroll
             for (int m = 0; m < kOM; ++m) {
@@ -770,14 +773,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     x[h] = o[nt][m][2 * h + e];
-                    // An infinity among the visible values meets a probability's residual, which may be 0 or negative:
-                    // a NaN. Where a sum is NaN and the weights are not (rare), the values say what it is.
-                    if constexpr (MOD)
-                        if (x[h] != x[h] && L == L) {
-                            const float f = sum_nonfinite<kPBF16>(p, b, kvh, P, DH, m * 16 + h * 8 + r0,
-                                                                  max(pc.key_begin, tok0), min(len, tok0 + pc.n * P));
-                            if (f != 0.f) x[h] = f;  // (0: finite values whose weighted sum left fp32)
-                        }
+                    if constexpr (MOD) nan |= x[h] != x[h];
                     x[h] = whole && L == 0.f ? 0.f : x[h] * scale;
                 }
                 if constexpr (kI8) {
@@ -787,8 +783,36 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                     dst[m * 16 + 8 + r0] = x[1];
                 }
             }
-            if (!whole && r0 == 0) p.part_ml[ps] = make_float2(m_col[nt][e], L);
+            if (!whole && r0 == 0) p.part_ml[partial(n)] = make_float2(m_col[nt][e], L);
         }
+    if constexpr (MOD) {
+        // An infinity among the visible values meets a probability's residual, which may be 0 or negative: a NaN. Where a
+        // sum is NaN and the weights are not (rare), the values say what it is. (After the stores, so that the sums need
+        // no registers beside the search.)
+        if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll 1
+            for (int m = 0; m < kOM; ++m) {
+                float x[16], f[2] = {0.f, 0.f};
+                sum_nonfinite16<kPBF16>(p, b, kvh, P, DH, m * 16, max(pc.key_begin, tok0), min(len, tok0 + pc.n * P), x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i == r0) f[0] = x[i], f[1] = x[8 + i];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int n = nt * 8 + 2 * quad + e;
+                        const float L = l_col[nt][e];
+                        if (n >= heads || !(L > 0.f)) continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float& y = out_row(n)[m * 16 + h * 8 + r0];
+                            if (y != y && f[h] != 0.f) y = whole ? f[h] / L : f[h];  // (0: finite values whose sum left fp32)
+                        }
+                    }
+            }
+        }
+    }
     }
 }
 

@@ -803,10 +803,18 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
         if constexpr (MOD) {
             // An infinity among the values the row sees meets a probability's residual, which may be 0 or negative:
             // a NaN. Where a sum is NaN and the weights are not (rare), the row's values say what it is.
-            if (U != U && L == L) {
+            // (A warp has 32 dims of one row; the sums are 0 for finite values whose weighted sum left fp32.)
+            if (__any_sync(0xffffffffu, U != U && L == L)) {
                 const int tr = hh / p.g, pos = len - n_q + t0 + tr;
-                const float f = sum_nonfinite<kBF16>(p, b, kvh, P, DH, d, first_key(p, qs0 + t0 + tr, pos), max(pos + 1, prefix));
-                if (f != 0.f) U = f;  // (0: finite values whose weighted sum left fp32)
+                const int lo = first_key(p, qs0 + t0 + tr, pos), hi = max(pos + 1, prefix);
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    float x[16];
+                    sum_nonfinite16<kBF16>(p, b, kvh, P, DH, (d & ~31) + 16 * k, lo, hi, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((d & 31) == 16 * k + i && U != U && L == L && x[i] != 0.f) U = x[i];
+                }
             }
         }
         if (!split_mode) {

@@ -65,8 +65,9 @@ struct PfCapCfg {
     // tile_full[4], tile_empty[4], summed[4]
     static constexpr int kNumBars = 2 * kRing + 12 + 6 + 3 * kTileSlots;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
-    static constexpr int kOffDirty = kOffTmem + 8;  // a stage seen in part held a NaN or an infinity in V
-    static constexpr int kOffMasks = kOffTmem + 16;
+    // [tile slot]: number + 1 of the last tile (with stages) of which a stage seen in part held a NaN or an infinity in V
+    static constexpr int kOffDirty = kOffTmem + 8;
+    static constexpr int kOffMasks = kOffDirty + 4 * kTileSlots;
     static constexpr int kOffNext = (kOffMasks + 4 * kMasks + 15) / 16 * 16;  // answer to the request for a tile
     static constexpr int kTileWords = 32 + 128;  // a tile's description and the first keys of its up to 128 tokens
     static constexpr int kOffTiles = kOffNext + 16;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(tile_empty(i), C::kThreads / 32 - 1);
             mbar_init(summed(i), C::kSoftmaxWarps);
         }
-        *dirty = 0;
+        for (int i = 0; i < C::kTileSlots; ++i) dirty[i] = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -501,7 +502,8 @@ __global__ void __launch_bounds__(512, 1)
             float l = 0.f;
 #pragma unroll
             for (int k = 0; k < kG; ++k) l += xl[(slot * kG + k) * 128 + r];
-            const bool search = *dirty != 0;
+            const bool search = dirty[slot] == read_out;  // (read_out is the tile's number + 1 by now)
+            bool nan = false;
             float* dst = p.out + last_row * DH + od;
             const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -522,35 +524,32 @@ __global__ void __launch_bounds__(512, 1)
                     for (int i = 0; i < 16; ++i) o[i] = 0.f;
                 }
                 if (last_row >= 0) {
-                    // NaN and infinities among the values this row sees (rare): those of stages seen in part were zeroed for
-                    // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
-                    // values, read again, say what those sums are.
-                    bool again = search;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) again = again || o[i] != o[i];
+                    for (int i = 0; i < 16; ++i) nan = nan || o[i] != o[i];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4*>(dst + q * 16 + i) =
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-                    if (again && l == l && ok) {
-                        const ChunkTile ct = chunk_tile(p, (n_tiles - 1 - last_tile) / p.H_kv);
-                        const int b = ct.b, kvh = last_tile % p.H_kv, i0 = ct.t0 + tr, len = p.seq_lens[b];
-                        const int pos = len - ct.n_q + i0;
-                        const int lo = first_key(p, ct.qs0 + i0, pos);
-                        const int hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[b], len) : 0);
-#pragma unroll 1
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<true>(p, b, kvh, P, DH, od + q * 16 + i, lo, hi);
-                            float& y = dst[q * 16 + i];
-                            if (x != 0.f) y = y != y ? x * inv : y + x * inv;  // (0: finite values whose weighted sum left fp32)
-                        }
-                    }
                 }
                 __syncwarp();  // the next load is warp-collective
             }
             release_o();
 #pragma unroll
             for (int i = 0; i < C::kDims / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            // NaN and infinities among the values this row sees (rare): those of stages seen in part were zeroed for the
+            // product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's values, read
+            // again, say what those sums are. (O is released before: P.V of the next tile waits for it.)
+            const bool again = last_row >= 0 && (search || nan) && l == l && l != 0.f && ok;
+            if (__any_sync(0xffffffffu, again)) {
+                const ChunkTile ct = chunk_tile(p, (n_tiles - 1 - last_tile) / p.H_kv, lane);
+                const int i0 = ct.t0 + tr, len = p.seq_lens[ct.b], pos = len - ct.n_q + i0;
+                int lo = 0, hi = 0;
+                if (again) {
+                    lo = first_key(p, ct.qs0 + i0, pos);
+                    hi = max(pos + 1, p.prefix_lens != nullptr ? min(p.prefix_lens[ct.b], len) : 0);
+                }
+                add_nonfinite<true>(p, ct.b, last_tile % p.H_kv, P, DH, od, min(od + C::kDims, DH), lo, hi, inv, dst);
+            }
             last_tile = -1;
         };
 
@@ -692,7 +691,8 @@ __global__ void __launch_bounds__(512, 1)
                         } else if (part) {
                             const uint4 v = lds128(at);
                             if (has_nonfinite16<true>(v)) {
-                                *dirty = 1;
+                                const int number = read_out + (last_tile >= 0 ? 1 : 0);
+                                dirty[number % C::kTileSlots] = number + 1;
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
                                              "r"(v.x ^ nonfinite16<true>(v.x)), "r"(v.y ^ nonfinite16<true>(v.y)),
                                              "r"(v.z ^ nonfinite16<true>(v.z)), "r"(v.w ^ nonfinite16<true>(v.w))

@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(384, 1)
         float* dst = p.out + qrow * DH + od;
         if (okl) {
             const float inv = l_all != 0.f ? 1.f / l_all : 0.f;
+            bool nan = false;
 #pragma unroll
             for (int q = 0; q < kH / 16; ++q) {
                 uint32_t a[16];
@@ -568,27 +569,21 @@ __global__ void __launch_bounds__(384, 1)
                         o[i] = __uint_as_float(a[i]) + acc[q * 8 + i / 2].x;
                         o[i + 1] = __uint_as_float(a[i + 1]) + acc[q * 8 + i / 2].y;
                     }
-                    // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for
-                    // the product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's
-                    // values, read again, say what those sums are.
-                    bool again = dirty;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) again = again || o[i] != o[i];
+                    for (int i = 0; i < 16; ++i) nan = nan || o[i] != o[i];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4*>(dst + q * 16 + i) =
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-                    if (again && l_all == l_all) {
-#pragma unroll 1
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = sum_nonfinite<kBF16>(p, b, kvh, P, DH, od + q * 16 + i, row_lo, row_hi);
-                            float& y = dst[q * 16 + i];
-                            if (x != 0.f) y = y != y ? x * inv : y + x * inv;  // (0: finite values whose weighted sum left fp32)
-                        }
-                    }
                 }
                 __syncwarp();  // the next load is warp-collective
             }
+            // NaN and infinities among the values this row sees (rare): those of boundary stages were zeroed for the
+            // product, and an infinity elsewhere times a residual of 0 gave a NaN. Either way the row's values, read
+            // again, say what those sums are.
+            const bool again = row_valid && (dirty || nan) && l_all == l_all && l_all != 0.f;
+            if (__any_sync(0xffffffffu, again))
+                add_nonfinite<kBF16>(p, b, kvh, P, DH, od, od + kH, again ? row_lo : 0, again ? row_hi : 0, inv, dst);
         } else if (row_valid) {
             for (int d = 0; d < kH; ++d) dst[d] = 0.f;
         }

@@ -52,17 +52,6 @@ __device__ __forceinline__ ChunkTile chunk_tile(const DecodeParams& p, int slot,
     }
     return tile_of(p, lo, slot);
 }
-// The same for one thread.
-__device__ __forceinline__ ChunkTile chunk_tile(const DecodeParams& p, int slot) {
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_slot(p, mid) <= slot) lo = mid;
-        else hi = mid;
-    }
-    return tile_of(p, lo, slot);
-}
-
 // Keys of a tile of nt query rows (chunk tokens) at positions pos0 ..: some row sees keys in [begin, end) only;
 // every row sees all keys in [all0, all1). Called by whole warps.
 struct TileKeys {
@@ -323,18 +312,80 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
                            __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))));
 }
 
-// Sum of the NaN and infinite elements of dim d of V over keys lo .. hi - 1 of sequence b (pages outside the pool
-// left out): what an attention sum over those keys is once it holds one.
+// x[i] = sum of the NaN and infinite elements of dim d0 + i of V over the keys lo .. hi - 1 that this lane's row of
+// sequence b sees (lo >= hi: none), pages outside the pool left out: what an attention sum over those keys is once it holds
+// one; 0 where there is none. Called by whole warps, which stand between other warps and their next stage: the lanes
+// search different keys, four each with their loads in flight together, and only keys that hold such an element are then
+// gone through by all of them. (A thread on its own, dim by dim and key by key, needs seconds for a context of 100,000
+// keys, and the waits for its warp end after one.)
 template <bool IS_BF16>
-__device__ __noinline__ float sum_nonfinite(const DecodeParams& p, int b, int kvh, int P, int DH, int d, int lo, int hi) {
-    float acc = 0.f;
-    for (int t = lo; t < hi; ++t) {
-        const int pg = p.block_tables[(int64_t)b * p.max_blocks + t / P];
-        if (pg < 0 || pg >= p.num_pages) continue;
-        const uint32_t v = static_cast<const uint16_t*>(p.v_pages)[(((int64_t)pg * p.H_kv + kvh) * P + t % P) * DH + d];
-        acc += unpack16<IS_BF16>(nonfinite16<IS_BF16>(v)).x;
+__device__ __noinline__ void sum_nonfinite16(const DecodeParams& p, int b, int kvh, int P, int DH, int d0, int lo, int hi,
+                                             float (&x)[16]) {
+    constexpr int kBatch = 4;
+    const uint32_t lane = threadIdx.x & 31;
+    const int lg = P == 16 ? 4 : 5;
+    const uint32_t first = __reduce_min_sync(0xffffffffu, lo < hi ? static_cast<uint32_t>(lo) : 0xffffffffu);
+    const uint32_t end = __reduce_max_sync(0xffffffffu, lo < hi ? static_cast<uint32_t>(hi) : 0u);
+    const int32_t* table = p.block_tables + (int64_t)b * p.max_blocks;
+    auto row = [&](uint32_t t) -> const uint4* {  // the sixteen elements of key t
+        const int pg = table[t >> lg];
+        if (pg < 0 || pg >= p.num_pages) return nullptr;
+        return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v_pages) +
+                                              ((((int64_t)pg * p.H_kv + kvh) << lg) + (t & (P - 1))) * DH + d0);
+    };
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    for (uint32_t t0 = first; t0 < end; t0 += 32 * kBatch) {
+        uint4 v[kBatch][2];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t t = t0 + 32 * k + lane;
+            const uint4* src = t < end ? row(t) : nullptr;
+            v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (src != nullptr) v[k][0] = src[0], v[k][1] = src[1];
+        }
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k) {
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (j == k) found = has_nonfinite16<IS_BF16>(v[j][0]) || has_nonfinite16<IS_BF16>(v[j][1]);
+            for (unsigned m = __ballot_sync(0xffffffffu, found); m != 0; m &= m - 1) {
+                const uint32_t t = t0 + 32 * k + __ffs(m) - 1;
+                if (t < static_cast<uint32_t>(lo) || t >= static_cast<uint32_t>(hi) || lo >= hi) continue;
+                const uint4* src = row(t);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 u = src[h];
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 e = unpack16<IS_BF16>(nonfinite16<IS_BF16>(w[i]));
+                        x[8 * h + 2 * i] += e.x;
+                        x[8 * h + 2 * i + 1] += e.y;
+                    }
+                }
+            }
+        }
     }
-    return acc;
+}
+
+// The same for dims d0 .. d1 - 1 (a multiple of sixteen) of this lane's output row, at dst from dim d0 on: a NaN there is an
+// infinity times a residual of 0, anything else lacks what was zeroed for the product. Sums of 0 (nothing found, or finite
+// values whose weighted sum left fp32) change nothing. inv: 1 / the row's sum of weights.
+template <bool IS_BF16>
+__device__ __noinline__ void add_nonfinite(const DecodeParams& p, int b, int kvh, int P, int DH, int d0, int d1, int lo,
+                                           int hi, float inv, float* dst) {
+    for (int d = d0; d < d1; d += 16) {
+        float x[16];
+        sum_nonfinite16<IS_BF16>(p, b, kvh, P, DH, d, lo, hi, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (x[i] == 0.f) continue;
+            float& y = dst[d - d0 + i];
+            y = y != y ? x[i] * inv : y + x[i] * inv;
+        }
+    }
 }
 
 }  // namespace kvp

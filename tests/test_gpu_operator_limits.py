@@ -147,3 +147,52 @@ def test_decode_mod_infinity_of_a_vanishing_weight(num_splits):
     ref, top = M._reference(c, q, np.arange(2), np.array(lens) - 1, 128**-0.5)
     assert (ref[:, :, 7] == -np.inf).all() and np.isfinite(np.delete(ref, 7, 2)).all()
     M._close(M._decode(c, q, 128**-0.5, num_splits), ref, top, "infinity")
+
+
+@pytest.mark.parametrize("num_splits", [1, 0])
+def test_decode_mod_infinity_in_a_long_row(num_splits):
+    """The search for what made a sum NaN does not hold up the waits of the same CTA, however long the row is."""
+    lens = [200000, 40, 90000]
+    c = M._cache(lens, 1, 128, 16, "bf16", seed=9)
+    q = torch.randn((3, 8, 128), generator=c["g"], device="cuda").to(torch.bfloat16)
+    for b, t, d, what in ((0, 5, 3, "inf"), (0, 199999, 127, "-inf"), (2, 45000, 64, "nan"), (2, 89000, 65, "inf")):
+        c["vp"][int(c["tab"][b, t // 16]), 0, t % 16, d] = float(what)
+    ref, top = M._reference(c, q, np.arange(3), np.array(lens) - 1, 128**-0.5, 30.0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    M._close(M._decode(c, q, 128**-0.5, num_splits, err=err, softcap=30.0), ref, top, "long row")
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype,Dh,kernel", PREFILL)
+def test_prefill_mod_infinities_in_many_tiles(dtype, Dh, kernel):
+    """Infinities that some tiles of one sequence see, in stages that all of a tile's rows see and in such that only some do:
+    every other row keeps its bits, those that see them say so, and no wait runs out, with many tiles a CTA and a long
+    context."""
+    lens, chunks = [70000, 9000, 12000], np.array([1400, 3000, 2500])
+    H_kv, g = 4, 4
+    c = M._cache(lens, H_kv, Dh, 16, dtype, seed=10)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b), H_kv * g, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    mod = dict(softcap=20.0)
+    ks = np.maximum(0, np.where(b == 2, pos - 2000, 0))
+    run = lambda err=None: _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, ks, err=err, **mod))  # noqa: E731
+    clean = run()
+    marks = [(0, 69000, 1, 5, "inf"), (0, 3, 2, 6, "-inf"), (0, 69001, 0, 7, "nan"), (2, 10500, 3, 8, "inf"), (2, 11999, 3, 9, "inf")]
+    for i, t, h, d, what in marks:
+        c["vp"][int(c["tab"][i, t // 16]), h, t % 16, d] = float(what)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(err)
+    assert int(err) == 0
+    want = clean.copy()
+    touched = np.zeros((len(b), H_kv * g), bool)
+    for i, t, h, d, what in marks:
+        sees = (b == i) & (pos >= t) & (ks <= t)
+        want[sees, h * g:(h + 1) * g, d] = float(what)
+        touched[sees, h * g:(h + 1) * g] = True
+    special = ~np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[special & ~np.isnan(want)], want[special & ~np.isnan(want)])
+    # the other dims of a row that sees one: the same but for the order of its sums
+    assert np.array_equal(got[~touched], clean[~touched])
+    other = touched[:, :, None] & ~special
+    assert np.abs(got[other] - clean[other]).max() <= 2.0**-13 * 6
