@@ -181,16 +181,16 @@ __global__ void __launch_bounds__(32 * (NW + 1), 2)
         if constexpr (MOD) {
             const ChunkTile ct = chunk_tile(p, (gridDim.x - 1 - blockIdx.x) / p.H_kv, threadIdx.x & 31);
             kvh = blockIdx.x % p.H_kv;
-            b = ct.b, qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
+            b = ct.b, qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0, nt = ct.nt;
         } else {
             kvh = blockIdx.y;
             b = blockIdx.z;
             qs0 = p.q_start[b];
             n_q = p.q_start[b + 1] - qs0;
             t0 = blockIdx.x * p.q_tile;
+            nt = min(p.q_tile, n_q - t0);
         }
-        if (t0 >= n_q) return;
-        nt = min(p.q_tile, n_q - t0);
+        if (nt <= 0) return;
     } else if (p.items != nullptr) {
         const int4 it = p.items[blockIdx.x];
         if (it.x < 0) return;

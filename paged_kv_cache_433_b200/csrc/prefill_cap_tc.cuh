@@ -98,7 +98,7 @@ __device__ __forceinline__ CapTile cap_tile(const DecodeParams& p, int tile, int
     t.qs0 = ct.qs0;
     const int n_q = ct.n_q, len = p.seq_lens[t.b];
     t.t0 = ct.t0;
-    t.nt = min(p.q_tile, n_q - t.t0);
+    t.nt = ct.nt;
     t.bad_len = len < 0 || len > p.max_blocks * P || n_q > len;
     t.pos0 = len - n_q + t.t0;
     t.prefix = p.prefix_lens != nullptr ? min(p.prefix_lens[t.b], len) : 0;

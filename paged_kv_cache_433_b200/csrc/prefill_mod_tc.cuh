@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(384, 1)
     const int kvh = blockIdx.x % p.H_kv, b = ct.b;
     const int g = p.g;
     const int qs0 = ct.qs0, n_q = ct.n_q, t0 = ct.t0;
-    if (t0 >= n_q) return;
-    const int nt = min(p.q_tile, n_q - t0);
+    const int nt = ct.nt;
+    if (nt <= 0) return;
     int len = p.seq_lens[b];
     auto zero_tile = [&]() {
         for (int e = threadIdx.x; e < nt * g * DH; e += blockDim.x) {

@@ -25,11 +25,11 @@ __device__ __forceinline__ int first_key(const DecodeParams& p, int row, int pos
 // The grids of the chunked prefill with modified scores: sequence b has the tile slots from q_start[b] / q_tile + b on, as
 // many as its rows can need, n_rows / q_tile + B in all whatever the chunks' lengths are. (A slot per sequence and tile of
 // the longest chunk, with one chunk of 4096 among 256: 262144 tiles, 1.8 ms for nothing.) Slots past a chunk's end have
-// t0 >= n_q. The grids run through the KV heads of a slot first and through the slots from the last one down: a prompt's
+// no rows. The grids run through the KV heads of a slot first and through the slots from the last one down: a prompt's
 // last tiles see the most keys, and a launch that ends with its small ones ends evenly (capped prefill, two prompts in
 // windowed documents: 251 us, 300 with a head's slots in ascending order behind one another).
 struct ChunkTile {
-    int b, qs0, n_q, t0;  // sequence, its first row, its rows; the tile's first row of them
+    int b, qs0, n_q, t0, nt;  // sequence, its first row, its rows; the tile's first row of them, and its rows (<= 0: none)
 };
 __device__ __forceinline__ int first_slot(const DecodeParams& p, int b) { return p.q_start[b] / p.q_tile + b; }
 __device__ __forceinline__ ChunkTile tile_of(const DecodeParams& p, int b, int slot) {
@@ -38,7 +38,8 @@ __device__ __forceinline__ ChunkTile tile_of(const DecodeParams& p, int b, int s
     t.qs0 = p.q_start[b];
     t.n_q = p.q_start[b + 1] - t.qs0;
     t.t0 = (slot - first_slot(p, b)) * p.q_tile;
-    if (t.t0 < 0) t.n_q = t.t0 = 0;  // (a first row other than 0)
+    if (t.t0 < 0 || t.qs0 < 0) t.n_q = t.t0 = t.qs0 = 0;  // (a first row other than 0)
+    t.nt = min(min(p.q_tile, t.n_q - t.t0), p.n_rows - t.qs0 - t.t0);  // no row past q and out, whatever q_start says
     return t;
 }
 // The tile in `slot`; called by whole warps: the last sequence whose slots begin no later, 32 candidates a step.
@@ -52,6 +53,7 @@ __device__ __forceinline__ ChunkTile chunk_tile(const DecodeParams& p, int slot,
     }
     return tile_of(p, lo, slot);
 }
+
 // Keys of a tile of nt query rows (chunk tokens) at positions pos0 ..: some row sees keys in [begin, end) only;
 // every row sees all keys in [all0, all1). Called by whole warps.
 struct TileKeys {

@@ -196,3 +196,26 @@ def test_prefill_mod_infinities_in_many_tiles(dtype, Dh, kernel):
     assert np.array_equal(got[~touched], clean[~touched])
     other = touched[:, :, None] & ~special
     assert np.abs(got[other] - clean[other]).max() <= 2.0**-13 * 6
+
+
+# ------------------------------------------------------------------ rows past n_rows
+@pytest.mark.parametrize("dtype,Dh,kernel", PREFILL)
+@pytest.mark.parametrize("n_rows,starts", [(10, [0, 40]), (33, [0, 30, 70]), (64, [0, 64, 90]), (50, [0, 5, 5, 49, 120])])
+def test_prefill_mod_rows_past_n_rows_are_left_alone(dtype, Dh, kernel, n_rows, starts):
+    """Chunks that reach past n_rows: their rows before it are computed, those past it not written."""
+    chunks = np.diff(starts)
+    lens = chunks + 100
+    c = M._cache(lens, 2, Dh, 16, dtype, seed=7)
+    b, pos, _ = M._rows(lens, chunks)
+    q = torch.randn((starts[-1], 8, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    ref, top = M._reference(c, q, b, pos, Dh**-0.5, 20.0, None, 64)
+    out = torch.full(q.shape, 7.0, device="cuda")  # (as large as the chunks: what a fault would write stays inside)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d_start, tab, d_len = M._d(starts), torch.from_numpy(c["tab"]).cuda(), M._d(lens)
+    _with_kernel(kernel, lambda: K.paged_prefill_attention_mod(
+        out[:n_rows], q[:n_rows], d_start, int(chunks.max()), c["kp"], c["vp"], tab, d_len, Dh**-0.5, softcap=20.0, window=64,
+        err_flag=err))
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    assert (got[n_rows:] == 7).all()
+    M._close(got[:n_rows], ref[:n_rows], top[:n_rows], "rows before n_rows")
