@@ -436,6 +436,13 @@ struct ColsLayout {
 
 constexpr int32_t kColsDirectTokens = 256;
 
+// Cuts, (m, l) and u of a balanced launch of L->grid CTAs.
+void balanced_offsets(ColsLayout* L, int64_t g, int32_t Dh) {
+    L->ml_off = sizeof(int4) * static_cast<size_t>(L->grid);
+    L->u_off = (L->ml_off + sizeof(float2) * 2 * static_cast<size_t>(L->grid) * g + 15) / 16 * 16;
+    L->bytes = L->u_off + sizeof(float) * 2 * static_cast<size_t>(L->grid) * g * Dh;
+}
+
 int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks, int32_t page_size, int32_t window,
                 int32_t num_splits, int kv_bytes, ColsLayout* out) {
     ColsLayout L;
@@ -457,9 +464,7 @@ int cols_layout(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_bl
         L.balanced = true;
         L.grid = static_cast<int32_t>(std::min<int64_t>(slots, (line + min_pages - 1) / min_pages));
         L.by_row = 4LL * B * H_kv < L.grid;
-        L.ml_off = sizeof(int4) * static_cast<size_t>(L.grid);
-        L.u_off = (L.ml_off + sizeof(float2) * 2 * static_cast<size_t>(L.grid) * g + 15) / 16 * 16;
-        L.bytes = L.u_off + sizeof(float) * 2 * static_cast<size_t>(L.grid) * g * Dh;
+        balanced_offsets(&L, g, Dh);
     } else {
         const int rc = resolve_splits(B, H_kv, max_blocks, num_splits, &L.S, &L.C, kv_bytes);
         if (rc != KV_OK) return rc;
@@ -625,8 +630,16 @@ int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32
         return KV_ERR_ARG;
     ColsLayout L;
     const int rc = cols_layout(B, H_q, H_kv, Dh, max_blocks, page_size, 0, num_splits, 2, &L);
-    if (rc == KV_OK) *out = L.bytes;
-    return rc;
+    if (rc != KV_OK) return rc;
+    *out = L.bytes;
+    const int64_t g = H_q / H_kv, span = kColsItemTokens / page_size + static_cast<int64_t>(max_blocks);
+    if (num_splits == 0 && B <= kColsMaxB && B * static_cast<int64_t>(H_kv) * span >= (1LL << 31)) {
+        // too long a line for a balanced launch, but not for one with a window
+        L.grid = sm_count() * (g <= 8 ? kColsCtas1 : 2);
+        balanced_offsets(&L, g, Dh);
+        *out = std::max(*out, L.bytes);
+    }
+    return KV_OK;
 }
 
 int paged_decode_launch_info(int32_t B, int32_t H_q, int32_t H_kv, int32_t Dh, int32_t max_blocks, int32_t page_size,

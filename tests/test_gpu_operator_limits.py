@@ -219,3 +219,25 @@ def test_prefill_mod_rows_past_n_rows_are_left_alone(dtype, Dh, kernel, n_rows, 
     got = out.double().cpu().numpy()
     assert (got[n_rows:] == 7).all()
     M._close(got[:n_rows], ref[:n_rows], top[:n_rows], "rows before n_rows")
+
+
+# ------------------------------------------------------------------ wide tables
+def test_decode_mod_workspace_of_the_widest_tables():
+    """paged_decode_ext_workspace_bytes holds for any window: also where the rows laid end to end leave 32 bits without a
+    window and not with one."""
+    B, H_kv, mb, P = 1024, 8, 262144, 16
+    c = M._cache([900] * 3, H_kv, 64, P, "bf16", seed=8)
+    tab = torch.full((B, mb), -1, dtype=torch.int32, device="cuda")
+    lens = np.zeros(B, int)
+    rows = np.array([0, 511, 1023])
+    lens[rows] = 900
+    tab[torch.from_numpy(rows).cuda(), :c["tab"].shape[1]] = torch.from_numpy(c["tab"]).cuda()
+    q = torch.randn((B, H_kv, 64), generator=c["g"], device="cuda").to(torch.bfloat16)
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    ws = torch.empty(max(16, K.paged_decode_ext_workspace_bytes(B, H_kv, H_kv, 64, mb, P)), dtype=torch.uint8, device="cuda")
+    K.paged_decode_attention_mod(out, q, c["kp"], c["vp"], tab, M._d(lens), 0.125, window=700, workspace=ws)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    ref, top = M._reference(c, q[torch.from_numpy(rows).cuda()], np.arange(3), np.full(3, 899), 0.125, 0.0, None, 700)
+    M._close(got[rows], ref, top, "wide table")
+    assert not np.delete(got, rows, 0).any()
