@@ -291,12 +291,13 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
         static_assert(32 % kPPG == 0, "page groups must tile the 32-entry table window");
         bool ok = true;
         int issued = 0;
-        while (ok && walk.next(pc)) {
+        while (walk.next(pc)) {
             if (p.cuts_by_row && lane == 0 && (pc.slot & 1)) {  // the row starts here: whole (-1) or cut (2c + 1)
                 const int64_t after = pre[pc.b] * p.H_kv + static_cast<int64_t>(pc.kvh + 1) * (pre[pc.b + 1] - pre[pc.b]);
                 const int c = blockIdx.x, pieces = static_cast<int>((after * G - 1) / T) - c + 1;
                 p.cuts[pc.b * p.H_kv + pc.kvh] = make_int4(pc.slot < 0 ? -1 : pc.b, pc.kvh, pieces, c);
             }
+            if (!ok) continue;  // a wait ran out: no load any more, but the merge finds every row's entry
             const int n_units = (pc.tokens(P) + C::kU - 1) / C::kU, n_st = (n_units + kUPS - 1) / kUPS;
             const int32_t* row = p.block_tables + (int64_t)pc.b * p.max_blocks + pc.page0;
             int tab = 0;  // block-table entry of page (first page of the group & ~31) + lane
