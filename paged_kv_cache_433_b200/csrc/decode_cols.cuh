@@ -754,11 +754,6 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         o[nt][m][2 * h + e] = o[nt][m][2 * h + e] * sa + src[((nt * kOM + m) * 4 + 2 * h + e) * kLanes] * sb;
             }
     }
-    const bool whole = pc.slot < 0;
-    auto partial = [&](int n) {  // slot of the slice's head n in the partials
-        return balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : ((int64_t)b * p.H_q + head0 + n) * p.num_splits + blockIdx.x;
-    };
-    auto out_row = [&](int n) { return whole ? p.out + ((int64_t)b * p.H_q + head0 + n) * DH : p.part_u + partial(n) * DH; };
     bool nan = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -766,7 +761,10 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
         for (int e = 0; e < 2; ++e) {
             const int n = nt * 8 + 2 * quad + e;
             if (n >= heads) continue;
-            float* dst = out_row(n);
+            const int64_t hq = (int64_t)b * p.H_q + head0 + n;
+            const bool whole = pc.slot < 0;
+            const int64_t ps = balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : hq * p.num_splits + blockIdx.x;
+            float* dst = whole ? p.out + hq * DH : p.part_u + ps * DH;
             const float L = l_col[nt][e], scale = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
 #pragma unroll
             for (int m = 0; m < kOM; ++m) {
@@ -784,7 +782,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                     dst[m * 16 + 8 + r0] = x[1];
                 }
             }
-            if (!whole && r0 == 0) p.part_ml[partial(n)] = make_float2(m_col[nt][e], L);
+            if (!whole && r0 == 0) p.part_ml[ps] = make_float2(m_col[nt][e], L);
         }
     if constexpr (MOD) {
         // An infinity among the visible values meets a probability's residual, which may be 0 or negative: a NaN. Where a
@@ -805,9 +803,13 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
                         const int n = nt * 8 + 2 * quad + e;
                         const float L = l_col[nt][e];
                         if (n >= heads || !(L > 0.f)) continue;
+                        const bool whole = pc.slot < 0;
+                        const int64_t hq = (int64_t)b * p.H_q + head0 + n;
+                        const int64_t ps = balanced ? (int64_t)pc.slot * p.g + hs * NT * 8 + n : hq * p.num_splits + blockIdx.x;
+                        float* dst = whole ? p.out + hq * DH : p.part_u + ps * DH;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float& y = out_row(n)[m * 16 + h * 8 + r0];
+                            float& y = dst[m * 16 + h * 8 + r0];
                             if (y != y && f[h] != 0.f) y = whole ? f[h] / L : f[h];  // (0: finite values whose sum left fp32)
                         }
                     }
