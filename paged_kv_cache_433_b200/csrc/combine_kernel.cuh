@@ -26,11 +26,14 @@ constexpr int kCombineWarps = 8;
 // first item come from the plan; rows with one chunk were written by the
 // decode kernel and are skipped, empty rows are zeroed here; partial s of
 // (b, query head h) sits at item t0 + s, row h of that item's [g][Dh] block.
+// The partials and out are not __restrict__: the decode kernel may still be
+// writing them when this one starts, so they are read by ordinary loads behind
+// the wait.
 // MOD: a row's pages are counted from its first visible key (window,
 // key_start), and a NaN sum gives a NaN row.
 template <int DH, int WPR, bool MOD = false>
 __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
-    float* __restrict__ out, const float* __restrict__ part_u, const float2* __restrict__ part_ml,
+    float* out, const float* part_u, const float2* part_ml,
     const int32_t* __restrict__ seq_lens, int32_t B, int32_t H_q, int32_t S, int32_t pages_per_split, int32_t P,
     int32_t max_blocks, const int32_t* __restrict__ plan, int32_t H_kv, int32_t window,
     const int32_t* __restrict__ key_start) {

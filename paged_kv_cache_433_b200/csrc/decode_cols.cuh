@@ -820,7 +820,8 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
 }
 
 // Merges the rows that a balanced launch cut, one CTA per entry of `cuts` (sequence, KV head, pieces, first CTA c): a
-// row's pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: the
+// row's pieces are in slots 2c + 1, 2 (c + 1), 2 (c + 2), ... (No pointer is __restrict__: the decode kernel before may still
+// be writing these buffers when this one starts, so they must be read by ordinary loads behind the wait.) Latency-bound: the
 // warps share out the heads of the row's group and, with fewer heads than warps, a head's pieces (a long row of a small
 // batch is cut into dozens); a lane sums Dh / 32 dims with the loads of a round of pieces issued before any is used,
 // relative to its warp's own maximum, and the warps of a head meet in shared memory. The host gives it few warps where
@@ -828,8 +829,7 @@ __global__ void __launch_bounds__((ColsCfg<KT, DH, P, NT, DUP>::kThreads), (Cols
 constexpr int kCombineColsWarps = 16;
 template <int DH>
 __global__ void __launch_bounds__(32 * kCombineColsWarps) paged_combine_cols_kernel(
-    float* __restrict__ out, const float* __restrict__ part_u, const float2* __restrict__ part_ml,
-    const int4* __restrict__ cuts, int32_t H_q, int32_t g) {
+    float* out, const float* part_u, const float2* part_ml, const int4* cuts, int32_t H_q, int32_t g) {
     constexpr int kD = DH / 32, kRound = 8;
     __shared__ float red_u[kCombineColsWarps][DH], red_m[kCombineColsWarps], red_l[kCombineColsWarps];
     grid_dependency_wait();

@@ -63,14 +63,13 @@ __device__ __forceinline__ uint4 quantise16(const float (&x)[16], int32_t cpr, u
 // of the measured copy rate, at a size where a launch's start and end weigh as much as its middle); 15.4 us with a thread
 // per K or V vector and the slot read first. CTAs of 128: with 256 the append and the read-back behind it take 26.4 us for
 // 25.9.
+// No pointer in this file is __restrict__: the kernel before may still be writing what one reads here when it starts
+// (programmatic launches), so everything is read by ordinary loads behind the wait.
 constexpr int kAppendThreads = 128;
 template <int DT>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_int8_kernel(uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
-                                                             float* __restrict__ scales, const uint4* __restrict__ k_new,
-                                                             const uint4* __restrict__ v_new, int64_t k_stride,
-                                                             int64_t v_stride, const int64_t* __restrict__ slots,
-                                                             int64_t per, int32_t H_kv, int32_t lg_cpr, int32_t P,
-                                                             int64_t num_slots, int* err) {
+__global__ void __launch_bounds__(kAppendThreads) kv_append_int8_kernel(
+    uint4* k_pages, uint4* v_pages, float* scales, const uint4* k_new, const uint4* v_new, int64_t k_stride, int64_t v_stride,
+    const int64_t* slots, int64_t per, int32_t H_kv, int32_t lg_cpr, int32_t P, int64_t num_slots, int* err) {
     constexpr int kVec = 16 / RopeVec<DT>::kN;  // source vectors per thread and row
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
@@ -122,9 +121,8 @@ __device__ __forceinline__ void widen16(const uint4& v, float s, uint4* dst) {
 // TB/s.
 template <int DT>
 __global__ void __launch_bounds__(256) kv_dequant_pages_int8_kernel(
-    uint4* __restrict__ k_out, uint4* __restrict__ v_out, const uint4* __restrict__ k_pages,
-    const uint4* __restrict__ v_pages, const float* __restrict__ scales, const int32_t* __restrict__ src,
-    const int32_t* __restrict__ dst, int32_t upp, int32_t cpr, int32_t P, int32_t num_pages, int32_t num_out, int* err) {
+    uint4* k_out, uint4* v_out, const uint4* k_pages, const uint4* v_pages, const float* scales, const int32_t* src,
+    const int32_t* dst, int32_t upp, int32_t cpr, int32_t P, int32_t num_pages, int32_t num_out, int* err) {
     constexpr int kVec = 16 / RopeVec<DT>::kN, kBatch = 4;
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
@@ -159,10 +157,8 @@ __global__ void __launch_bounds__(256) kv_dequant_pages_int8_kernel(
 
 // Page copy with scales: 16-byte words of the K codes, the V codes and the
 // scales of every pair.
-__global__ void __launch_bounds__(256) kv_copy_pages_int8_kernel(uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
-                                                                 uint4* __restrict__ scales,
-                                                                 const int32_t* __restrict__ src,
-                                                                 const int32_t* __restrict__ dst, int32_t n,
+__global__ void __launch_bounds__(256) kv_copy_pages_int8_kernel(uint4* k_pages, uint4* v_pages, uint4* scales,
+                                                                 const int32_t* src, const int32_t* dst, int32_t n,
                                                                  int32_t code_words, int32_t scale_words,
                                                                  int32_t num_pages, int* err) {
     grid_dependency_wait();
@@ -174,8 +170,9 @@ __global__ void __launch_bounds__(256) kv_copy_pages_int8_kernel(uint4* __restri
             continue;
         }
         for (int32_t w = threadIdx.x; w < code_words; w += blockDim.x) {
-            k_pages[d * code_words + w] = k_pages[s * code_words + w];
-            v_pages[d * code_words + w] = v_pages[s * code_words + w];
+            const uint4 k = k_pages[s * code_words + w], v = v_pages[s * code_words + w];
+            k_pages[d * code_words + w] = k;
+            v_pages[d * code_words + w] = v;
         }
         for (int32_t w = threadIdx.x; w < scale_words; w += blockDim.x)
             scales[d * scale_words + w] = scales[s * scale_words + w];

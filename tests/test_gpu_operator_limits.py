@@ -5,6 +5,7 @@ import pytest
 import test_gpu_score_mod as M
 import torch
 
+from oracle import score_mod as O
 from paged_kv_cache_433_b200 import kvpaged as K
 
 pytestmark = pytest.mark.gpu
@@ -241,3 +242,60 @@ def test_decode_mod_workspace_of_the_widest_tables():
     ref, top = M._reference(c, q[torch.from_numpy(rows).cuda()], np.arange(3), np.full(3, 899), 0.125, 0.0, None, 700)
     M._close(got[rows], ref, top, "wide table")
     assert not np.delete(got, rows, 0).any()
+
+
+# ------------------------------------------------------------------ one launch behind another
+@pytest.mark.parametrize("graph", [False, True])
+def test_int8_calls_behind_one_another_read_what_the_last_one_wrote(graph):
+    """Norm + rotation into k_out, the append of it, a copy of its pages, the read-back and a decode whose rows are cut between
+    CTAs, step after step over the same buffers with other values: every launch reads what the one before has just written,
+    although it may have started before that one ended."""
+    T, H_q, H_kv, Dh, P, n = 4096, 8, 2, 128, 16, 256
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.empty((T, H_kv, Dh), dtype=torch.bfloat16, device="cuda")
+    v, k_out = torch.empty_like(x), torch.empty_like(x)
+    cos_sin = torch.cat([torch.ones((4, Dh // 2)), torch.zeros((4, Dh // 2))], 1).cuda()  # no rotation
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros((2 * n, H_kv, P, Dh), dtype=torch.int8, device="cuda") for _ in range(2))
+    sc = torch.zeros((2 * n, H_kv, 2, P), device="cuda")
+    ko, vo = (torch.zeros((n, H_kv, P, Dh), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.arange(T, device="cuda")
+    lo, hi = (torch.arange(i, i + n, dtype=torch.int32, device="cuda") for i in (0, n))
+    tab = hi[None].contiguous()
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, H_q, Dh), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.zeros((1, H_q, Dh), device="cuda")
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def step():
+        K.kv_norm_rope_append(None, None, x, None, None, pos, cos_sin, None, 1e-6, P, k_out=k_out)
+        K.kv_append_int8(kp, vp, sc, k_out, v, slots, P)
+        K.kv_copy_pages_int8(kp, vp, sc, lo, hi)
+        K.kv_dequant_pages_int8(ko, vo, kp, vp, sc, hi, lo)
+        K.paged_decode_attention_int8(out, q, kp, vp, sc, tab, lens, Dh**-0.5, workspace=ws)
+
+    x.normal_(generator=g), v.normal_(generator=g)
+    step()
+    torch.cuda.synchronize()
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            step()
+            step()
+    for i in range(20):
+        x.normal_(generator=g), v.normal_(generator=g)
+        v.mul_(2.0 ** (i % 5))
+        if graph:
+            cg.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        rows = lambda t: t.transpose(1, 2).reshape(T, H_kv, Dh).float().cpu().numpy()  # noqa: E731
+        for got, new in ((ko, k_out), (vo, v)):
+            codes, scales = O.quantise_int8(new.float().cpu().numpy())
+            want = torch.from_numpy(codes.astype(np.float32) * scales[..., None]).to(torch.bfloat16).float().numpy()
+            assert np.array_equal(rows(got), want), f"step {i}"
+        kd, vd = (rows(t.float()).astype(np.float64) for t in (ko, vo))
+        ref = O.attend_row(q[0].double().cpu().numpy(), kd, vd, T - 1, T, Dh**-0.5)
+        # the pages read back are rounded to bf16 (2^-9 of K and of V), their codes are not: scores up to 6 err by 6 * 2^-9
+        assert np.abs(out[0].double().cpu().numpy() - ref).max() <= (2 * 6 * 2.0**-9 + 2.0**-9) * np.abs(vd).max(), f"step {i}"
