@@ -513,13 +513,14 @@ int paged_decode_attention_mod(float* out, const void* q, const void* k_pages, c
                                const int32_t* key_start, int32_t num_splits, void* workspace, size_t ws_bytes,
                                int* err_flag, void* stream);
 
-/* Chunk form: rows, q_start, max_q_len and errors as paged_prefill_attention;
- * n_rows: rows of q and out, at least q_start[B] (it sizes the grid, by which
- * chunks of very different lengths in one call cost nothing; rows past it are
- * not computed). (A bidirectional prefix may reach behind the chunk's rows, never behind
- * seq_lens[b].) tcgen05 kernels for Dh = 128 and groups that divide 128 under
- * AUTO and TCGEN05 (one of its own for bf16 under a cap of at most 50 without
- * slopes), the warp-MMA kernel otherwise. Results repeat bit for bit. */
+/* Chunk form: rows, q_start and errors as paged_prefill_attention. n_rows: rows
+ * of q and out, at least q_start[B]; max_q_len: at least every chunk's rows (rows
+ * past either are not computed). n_rows sizes the grid, by which chunks of very
+ * different lengths in one call cost nothing. (A bidirectional prefix may reach
+ * behind the chunk's rows, never behind seq_lens[b].) tcgen05 kernels for Dh = 128
+ * and groups that divide 128 under AUTO and TCGEN05 (one of its own for bf16 under
+ * a cap of at most 50 without slopes), the warp-MMA kernel otherwise. Results
+ * repeat bit for bit. */
 int paged_prefill_attention_mod(float* out, const void* q, const int32_t* q_start, int32_t max_q_len, int32_t n_rows,
                                 const void* k_pages, const void* v_pages, const int32_t* block_tables,
                                 int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,

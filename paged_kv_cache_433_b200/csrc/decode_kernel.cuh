@@ -87,7 +87,7 @@ struct DecodeParams {
     const float* alibi_slopes;  // [H_q] (nullable): bias -slope * |query position - key position|
     const int32_t* key_start;   // first visible key per query row (nullable)
     const int32_t* prefix_lens; // multi-token query: keys visible to every row of sequence b (nullable)
-    int32_t n_rows;             // multi-token query, modified scores: rows of q and out
+    int32_t n_rows, max_q_len;  // multi-token query, modified scores: rows of q and out, and of a chunk, that are computed
     int32_t window;             // keys visible before and at the row's own position (0: all)
 };
 

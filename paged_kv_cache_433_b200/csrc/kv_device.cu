@@ -1056,6 +1056,7 @@ int prefill_impl(float* out, const void* q, const int32_t* q_start, int32_t max_
         set_mod(p, scale, mod->softcap, mod->alibi_slopes, mod->window, mod->key_start);
         p.prefix_lens = mod->prefix_lens;
         p.n_rows = mod->n_rows;
+        p.max_q_len = max_q_len;
         // A cap bounds every score by cap_out; where 2^(2 cap_out) fits fp32's range with room on both sides (bf16
         // operands have that range too) and no bias moves the scores, one reference serves all rows: no row maximum is
         // taken.

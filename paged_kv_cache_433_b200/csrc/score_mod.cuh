@@ -39,7 +39,8 @@ __device__ __forceinline__ ChunkTile tile_of(const DecodeParams& p, int b, int s
     t.n_q = p.q_start[b + 1] - t.qs0;
     t.t0 = (slot - first_slot(p, b)) * p.q_tile;
     if (t.t0 < 0 || t.qs0 < 0) t.n_q = t.t0 = t.qs0 = 0;  // (a first row other than 0)
-    t.nt = min(min(p.q_tile, t.n_q - t.t0), p.n_rows - t.qs0 - t.t0);  // no row past q and out, whatever q_start says
+    // no row past max_q_len, and none past q and out whatever q_start says
+    t.nt = min(min(p.q_tile, min(t.n_q, p.max_q_len) - t.t0), p.n_rows - t.qs0 - t.t0);
     return t;
 }
 // The tile in `slot`; called by whole warps: the last sequence whose slots begin no later, 32 candidates a step.

@@ -222,6 +222,20 @@ def test_prefill_mod_rows_past_n_rows_are_left_alone(dtype, Dh, kernel, n_rows, 
     M._close(got[:n_rows], ref[:n_rows], top[:n_rows], "rows before n_rows")
 
 
+@pytest.mark.parametrize("dtype,Dh,kernel", PREFILL)
+def test_prefill_mod_rows_past_max_q_len_are_left_alone(dtype, Dh, kernel):
+    lens, chunks = [200, 150, 90], np.array([70, 48, 90])
+    c = M._cache(lens, 2, Dh, 16, dtype, seed=7)
+    b, pos, start = M._rows(lens, chunks)
+    q = torch.randn((len(b), 8, Dh), generator=c["g"], device="cuda").to(M.DT[dtype])
+    ref, top = M._reference(c, q, b, pos, Dh**-0.5, 20.0)
+    out = torch.full(q.shape, 7.0, device="cuda")
+    got = _with_kernel(kernel, lambda: M._prefill(c, q, chunks, Dh**-0.5, max_q_len=48, out=out, softcap=20.0))
+    past = np.arange(len(b)) - start[b] >= 48
+    assert (got[past] == 7).all()
+    M._close(got[~past], ref[~past], top[~past], "rows before max_q_len")
+
+
 # ------------------------------------------------------------------ wide tables
 def test_decode_mod_workspace_of_the_widest_tables():
     """paged_decode_ext_workspace_bytes holds for any window: also where the rows laid end to end leave 32 bits without a
