@@ -54,15 +54,16 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
     // for the partials, from L2 (ld.global.cg), never from a line an earlier kernel left in this SM's L1.
     int len = 0;
     if (live) len = __ldcg(seq_lens + item / H_q);
+    const bool planned = !MOD && plan != nullptr;  // (modified scores have no such plan)
     auto row_pages = [&]() {  // pages of the row that the decode kernel read
         int n_pages = (len + P - 1) / P;
         if constexpr (MOD)
             n_pages -= min(first_visible_key(len - 1, window, key_start, static_cast<int>(item / H_q)), len) / P;
         return n_pages;
     };
-    int ns = plan != nullptr ? 0 : S;  // splits loaded (grid split: the row's own count masks them after)
+    int ns = planned ? 0 : S;  // splits loaded (grid split: the row's own count masks them after)
     int64_t base = item * S, stride = 1;
-    if (live && plan != nullptr) {
+    if (live && planned) {
         const int b = static_cast<int>(item / H_q);
         if (len < 0 || len > max_blocks * P) len = 0;
         const int n_pages = row_pages();
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(
                 for (int i = 0; i < kD; ++i) v[j][i] = 0.f;
             }
         }
-        if (plan == nullptr && r0 == 0) {
+        if (!planned && r0 == 0) {
             if (len < 0 || len > max_blocks * P) len = 0;
             const int n_pages = live ? row_pages() : 0;
             nrow = min(S, (n_pages + pages_per_split - 1) / pages_per_split);
