@@ -495,7 +495,9 @@ int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32
  * among the scores or values it sees gives NaN, an infinity among the values
  * its sign. Weighted sums are fp32, of weights up to 2^8 (2^50 in the chunk
  * form's kernel for bf16 under a cap of at most 50): where the |V| of a dim that
- * a row sees add up to more than 2^119 (2^77), it may come out infinite or NaN.
+ * a row sees add up to more than 2^119 (2^77), it may come out infinite or NaN,
+ * and in that kernel a row whose scores all lie near -50 loses bits of values
+ * below 2^-20.
  * Pages before the first visible key are not read (their table entries may be
  * anything).
  * softcap: 0 (none) or positive and finite (above 1e36 as none); window: 0 (none) or positive.

@@ -12,7 +12,7 @@
 // output, so that three CTAs of four consumer warps run on an SM. That
 // matters most for int8, whose warps are bound by latencies: 64 sequences of
 // 512..4096 tokens of an 8B-shaped layer (32 heads on 8, Dh = 128) took 81 us
-// with heads as rows and 8 consumer warps an SM, and take 61 us.
+// with heads as rows and 8 consumer warps an SM, and take 62 us.
 //
 // int8: the K codes are the first product's operand as they are (m16n8k32 of
 // signed bytes, 32-bit sums, exact); a query row, behind a power of two, is an
@@ -45,12 +45,13 @@
 // one (KV_DEV_ERR_PAGE_RANGE).
 //
 // Measured (8B-shaped layer, time of the whole call on the GPU, of the measured
-// copy rate): 16-bit, capped, 64 sequences of 512..4096 tokens 69 us, 5.77 TB/s
-// (0.88); 256 of 16..8192 with document masks and a distance bias 66 us (0.77,
-// the lengths' spread and the merge); int8, those 64: 61 us, 4.25 TB/s (0.65:
+// copy rate): 16-bit, capped, 64 sequences of 512..4096 tokens 69 us, 5.76 TB/s
+// (0.88); 256 of 16..8192 with document masks and a distance bias 65 us (0.78,
+// the lengths' spread and the merge); int8, those 64: 62 us, 4.18 TB/s (0.64:
 // its loads alone take 47 us; scales, integer products and widening share the
-// issue slots); int8, one sequence of 32768: 26 us (0.40: 444 CTAs' start and
-// the merge of one row's 55 pieces).
+// issue slots); int8, one sequence of 32768: 26 us (0.41: 444 CTAs' start and
+// the merge of one row's 55 pieces). Groups above 8 heads spill at Dh = 128:
+// int8, 128 heads on 8, 125 us for the 64 sequences.
 #pragma once
 
 #include <cuda.h>

@@ -14,8 +14,8 @@
 // vectors, position and slot are loaded before the current one is finished,
 // which doubles the bytes in flight of a launch that is bound by memory.
 // Everything between the load and the store is fp32.
-// Measured, 32 query and 8 KV heads of 128 (fp16): 8192 tokens 45 us, 4.6 TB/s
-// (0.70 of the measured copy rate, as kv_rope_append); 64 tokens 2.5 us, bound
+// Measured, 32 query and 8 KV heads of 128 (fp16): 8192 tokens 45 us, 4.5 TB/s
+// (0.69 of the measured copy rate, as kv_rope_append); 64 tokens 2.5 us, bound
 // by the launch and one round trip to memory.
 #include <cuda_runtime.h>
 

@@ -19,11 +19,13 @@
 // ahead into it, and a warpgroup computes its first stage of it before it reads out O of the last one, for which it has to
 // wait for the slowest. A tile's start and end, about 10 us with a CTA each, are hidden that way -- windowed layers have few stages per tile.
 //
-// Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 430 us, 680 TFLOP/s counted once, 1020 with the
-// residuals' products (a CTA per tile: 475 us; without the cap, prefill_tc.cuh: 425-430). Two prompts of 4096 tokens in
-// documents of 1500 under a window of 1024, cap 30: 260 us (a CTA per tile, ascending: 340). Bound by the chain Q K^T -> softmax ->
-// P V of a stage, about 10,400 cycles at three stages in flight: the matrix pipe is busy for 1,536 cycles a stage, the
-// exponentials for 1,024, and tensor memory has no room for a fourth buffer of scores.
+// Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 450 us at 1965 MHz, 650 TFLOP/s counted once, 975 with
+// the residuals' products; 489 us back to back, where the power cap holds the clock at 1700 MHz (a CTA per tile took a
+// tenth more; without the cap, prefill_tc.cuh: 425-430). Two prompts of 4096 tokens in documents of 1500 under a window of
+// 1024, cap 30: 252 us (a CTA per tile, ascending: a third more). That is for scores below a fifth of the cap; 1290 us
+// where many are above it (deviation 5) and 1980 at deviation 15, by the short loop in the softmax below. Bound by the
+// chain Q K^T -> softmax -> P V of a stage, about 10,400 cycles at three stages in flight: the matrix pipe is busy for
+// 1,536 cycles a stage, the exponentials for 1,024, and tensor memory has no room for a fourth buffer of scores.
 //
 // O is moved into fp32 sums in registers every kFlushKeys keys (score_mod.cuh). V rows that no row of the tile sees are
 // zeroed, and in a stage that some rows see only in part NaN and infinities too; the rows that do see them add them from
