@@ -500,7 +500,8 @@ int paged_decode_ext_workspace_bytes(int32_t B, int32_t H_q, int32_t H_kv, int32
  * below 2^-20.
  * Pages before the first visible key are not read (their table entries may be
  * anything).
- * softcap: 0 (none) or positive and finite (above 1e36 as none); window: 0 (none) or positive.
+ * softcap: 0 (none) or positive and finite (above 1e18 |scale| as none); window: 0
+ * (none) or positive.
  * bf16 / fp16 K/V, H_q / H_kv <= 64, Dh in {64, 128}, page_size in {16, 32},
  * num_pages * H_kv * page_size < 2^31. */
 

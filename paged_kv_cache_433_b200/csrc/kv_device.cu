@@ -487,7 +487,7 @@ int check_mod(float softcap, int32_t window) {
 // Coefficients poly[k] (scale / c)^2k scale log2 e of the capped score as a polynomial in the square of the product
 // x = q . k (score_mod.cuh), and the largest |x| that they serve (negative: none): |u| = |x scale / c| <= top. Under a
 // large cap the powers of scale / c leave fp32's range one after another; coefficients below it are left out, and the
-// polynomial then serves only |u| whose omitted terms are below 3e-8 of the score. x^2 has to stay in range as well.
+// polynomial then serves only |u| whose omitted terms are below 3e-8 of the score.
 float cap_poly(double scale, double c, const double* poly, int n, double top, float* coef) {
     const double u = scale / c;
     double f = scale * 1.4426950408889634;
@@ -499,16 +499,17 @@ float cap_poly(double scale, double c, const double* poly, int n, double top, fl
         ok = ok && a < 1e30 && (k > 0 || !out);
         if (out && k > 0) top = std::min(top, std::pow(3e-8 / std::abs(poly[k]), 0.5 / k));
     }
-    return ok ? static_cast<float>(std::min(top / std::abs(u), 1e18)) : -1.f;
+    return ok ? static_cast<float>(top / std::abs(u)) : -1.f;
 }
 
 void set_mod(DecodeParams& p, float scale, float softcap, const float* alibi_slopes, int32_t window,
              const int32_t* key_start) {
-    // a cap above 1e36 (scale / c may leave fp32's range) changes no score below 1e35
-    if (softcap > 0.f && softcap <= 1e36f) {
-        constexpr double kMax = 3.4e38;
+    // A cap above kCapNone |scale| changes no digit of the score of a product below 4e14, and of larger ones fp32 leaves
+    // differences of millions and more. (A product squared stays in fp32's range below it, too.)
+    constexpr double kCapNone = 1e18, kMax = 3.4e38;
+    if (softcap > 0.f && softcap <= kCapNone * std::abs(static_cast<double>(scale))) {
         p.cap_in = static_cast<float>(std::clamp(static_cast<double>(scale) / softcap, -kMax, kMax));
-        p.cap_out = std::max(softcap * kLog2e, 1.2e-38f);  // (0 would mean none)
+        p.cap_out = std::max(static_cast<float>(std::min(softcap * 1.4426950408889634, kMax)), 1.2e-38f);  // (0 would mean none)
         p.cap_small = cap_poly(scale, softcap, kTanhPoly, kCapTerms, kTanhSmall, p.cap_coef);
         p.cap_tiny = cap_poly(scale, softcap, kTanhTinyPoly, kCapTinyTerms, kTanhTiny, p.cap_coef_tiny);
     }

@@ -22,8 +22,8 @@
 // Measured, 32 heads on 8: 8 chunks of 512 tokens over 4096, cap 50: 450 us at 1965 MHz, 650 TFLOP/s counted once, 975 with
 // the residuals' products; 489 us back to back, where the power cap holds the clock at 1700 MHz (a CTA per tile took a
 // tenth more; without the cap, prefill_tc.cuh: 425-430). Two prompts of 4096 tokens in documents of 1500 under a window of
-// 1024, cap 30: 252 us (a CTA per tile, ascending: a third more). That is for scores below a fifth of the cap; 1290 us
-// where many are above it (deviation 5) and 1980 at deviation 15, by the short loop in the softmax below. Bound by the
+// 1024, cap 30: 252 us (a CTA per tile, ascending: a third more). That is for scores below a fifth of the cap; 1283 us
+// where many are above it (deviation 5) and 1841 at deviation 15, by the short loop in the softmax below. Bound by the
 // chain Q K^T -> softmax -> P V of a stage, about 10,400 cycles at three stages in flight: the matrix pipe is busy for
 // 1,536 cycles a stage, the exponentials for 1,024, and tensor memory has no room for a fourth buffer of scores.
 //

@@ -25,8 +25,8 @@
 //     memory, and the epilogue of such a tile adds them, read again from the
 //     pool, to the rows that do.
 // Measured, 32 heads on 8, 8 chunks of 512 tokens over 4096, back to back: bf16
-// without a cap 551 us (216 under a window of 1024), with slopes 654; fp16 under
-// a cap of 50 627, and 1990 where many scores pass a fifth of it (scalar forms of
+// without a cap 555 us (217 under a window of 1024), with slopes 657; fp16 under
+// a cap of 50 629, and 1770 where many scores pass a fifth of it (scalar forms of
 // the tanh). Bound by the chain of a stage, as prefill_cap_tc.cuh, and a tile's
 // start and end.
 // Every wait is bounded (KV_DEV_ERR_TIMEOUT); block-table entries outside

@@ -103,15 +103,11 @@ constexpr double kTanhPoly[kCapTerms] = {0.999999971, -0.333329589, 0.13325406, 
 constexpr int kCapTinyTerms = 3;
 constexpr double kTanhTiny = 0.2;
 constexpr double kTanhTinyPoly[kCapTinyTerms] = {0.999999895, -0.333285909, 0.130154075};
-// tanh(u) of any u: beyond kTanhSmall 1 - 2 / (1 + e^2u), whose error is 1e-7 of 1 (+-inf give +-1). That would be
-// anything but small beside a small u, which a cap far above the scores makes of all of them; the polynomial is there too.
-__device__ __forceinline__ float tanh_any(float u) {
-    constexpr float c[kCapTerms] = {kTanhPoly[0], kTanhPoly[1], kTanhPoly[2], kTanhPoly[3], kTanhPoly[4], kTanhPoly[5]};
-    const float z = u * u;
-    float r = c[kCapTerms - 1];
-#pragma unroll
-    for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, c[i]);
-    return fabsf(u) <= static_cast<float>(kTanhSmall) ? u * r : 1.f - 2.f * __frcp_rn(1.f + exp2f(u * 2.885390081777927f));
+// tanh(u) = 1 - 2 / (1 + e^2u): an error of 1e-7 of 1 (+-inf give +-1), for what the polynomials do not serve. Beside a small
+// u that is much, so the host keeps such u away: p.cap_small covers all up to kTanhSmall, under caps above about 500 (whose
+// coefficients leave fp32's range one after another) all up to 0.3, 0.17, 0.09 or 0.02, and a cap far above that is none.
+__device__ __forceinline__ float tanh_large(float u) {
+    return 1.f - 2.f * __frcp_rn(1.f + exp2f(u * 2.885390081777927f));
 }
 // Chunked prefill: the largest cap (log2 units; 50 in natural ones) with one softmax reference for all rows, and the
 // largest power of two that its probabilities then reach: they lie in 2^-96 .. 2^50, a residual of 16-bit splitting 2^9
@@ -149,8 +145,8 @@ __device__ __forceinline__ void cap_scores(const DecodeParams& p, const CapCoef&
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
                 const float2 t = cap_small2(k, make_float2(x[c], x[c + 1]));
-                x[c] = fabsf(x[c]) <= p.cap_small ? t.x : tanh_any(x[c] * p.cap_in) * p.cap_out;
-                x[c + 1] = fabsf(x[c + 1]) <= p.cap_small ? t.y : tanh_any(x[c + 1] * p.cap_in) * p.cap_out;
+                x[c] = fabsf(x[c]) <= p.cap_small ? t.x : tanh_large(x[c] * p.cap_in) * p.cap_out;
+                x[c + 1] = fabsf(x[c + 1]) <= p.cap_small ? t.y : tanh_large(x[c + 1] * p.cap_in) * p.cap_out;
             }
         } else {
 #pragma unroll
@@ -246,7 +242,7 @@ __device__ __forceinline__ void cap_row_any(const DecodeParams& p, const CapRowC
 #pragma unroll
         for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, p.cap_coef[i]);
         const float y = FIXED ? fmaf(x, r, k.neg_ref.x) : x * r;
-        return !large || fabsf(x) <= p.cap_small ? y : tanh_any(x * p.cap_in) * p.cap_out - (FIXED ? p.fixed_ref : 0.f);
+        return !large || fabsf(x) <= p.cap_small ? y : tanh_large(x * p.cap_in) * p.cap_out - (FIXED ? p.fixed_ref : 0.f);
     };
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
